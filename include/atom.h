@@ -396,6 +396,138 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
                                        void *out, atom_stream_t stream);
 
 /*
+ * Paged INT4 KV cache -- the cache of atom_kv_quant in pages, with what a
+ * serving step does to it: atom_kv4_append writes new tokens, atom_kv4_attention
+ * reads it, atom_kv4_attention_weights sums the weight that its tokens receive,
+ * atom_kv4_evict drops the tokens that received least, and atom_kv4_gather reads
+ * tokens back. The pages place Atom under KV-cache quantization ("Atom: Low-bit
+ * Quantization for Efficient and Accurate LLM Serving", key facts); the layout
+ * and the operators are this library's.
+ *
+ * atom_kv4_cache_t -- keys and values of `heads` KV heads in `pages` pages of
+ * `page_size` tokens. The vector of (page, slot, head) is number
+ *   v = page * page_stride + slot * token_stride + head * head_stride;
+ * its 64 bytes of codes are at k4 + 64 v (v4 + 64 v), its scale is ks[v]
+ * (vs[v]), both as atom_kv_quant writes them. A contiguous cache
+ * [tokens][heads][128] quantized by atom_kv_quant is one page (page_stride any,
+ * token_stride heads, head_stride 1). Any strides >= 0 are taken; writing to
+ * vectors that coincide is the caller's error. k4, v4 16-byte aligned, ks, vs
+ * 4-byte.
+ *
+ * atom_kv4_batch_t -- the sequences of a call, in device memory:
+ *   block_table  int32 [batch][table_stride]: the first max_pages entries of row
+ *                b are the pages of sequence b, in order. Entries behind its last
+ *                token's are not read.
+ *   kv_lens      int32 [batch]: cached tokens of a sequence, the call's new ones
+ *                included (they are its last).
+ *   cu_q         int32 [batch + 1]: rows cu_q[b] .. cu_q[b+1] - 1 of the call's
+ *                row tensors are the new tokens of sequence b. Rows behind
+ *                cu_q[batch] (padding) are neither read nor written.
+ *   max_q        host bound on cu_q[b+1] - cu_q[b]; picks the kernels of
+ *                atom_kv4_attention.
+ * A sequence whose entries contradict the call (cu_q descending or above the
+ * rows, more than max_q new tokens in atom_kv4_attention, kv_lens negative or
+ * above max_pages * page_size) is skipped, a page outside [0, pages) is not
+ * touched (attention reads its tokens as zeros), and either sets the device
+ * status to ATOM_ERR_INVALID_ARG.
+ *
+ * atom_kv4_append: k, v fp16 [rows][heads][128] with token and head strides in
+ *   elements -> codes and scales in the slots of positions kv_lens[b] - qn ..
+ *   kv_lens[b] - 1 (qn = cu_q[b+1] - cu_q[b] <= kv_lens[b]), bit for bit those
+ *   of atom_kv_quant. k, v 16-byte aligned, strides multiples of 8.
+ * atom_kv4_gather: the inverse; k_out, v_out fp16 [rows][heads][128], values as
+ *   atom_kv_dequant's.
+ *
+ * atom_kv4_attention: q fp16 [rows][q_heads][128] (token and head strides as
+ *   above; q_heads a multiple of heads, query head j reads KV head
+ *   j / (q_heads / heads)). For new token i of a sequence with qn of them,
+ *     s[t] = scale * sum_d q[d] k[t][d]   for t < limit,
+ *     limit = kv_len, or with causal != 0: kv_len - qn + i + 1,
+ *     lse = log sum_t exp(s[t]),  out = fp16( sum_t exp(s[t] - lse) v[t] ),
+ *   with k, v = code * scale unrounded. limit <= 0: out 0, lse -infinity.
+ *   out fp16 [rows][q_heads][128], lse fp32 [rows][q_heads] or NULL.
+ *   workspace: scratch that lets a sequence's cached tokens be shared between
+ *   CTAs; at least atom_kv4_attention_workspace_bytes(rows, q_heads, heads,
+ *   max_q), 16-byte aligned, contents irrelevant before and after. NULL, or
+ *   fewer bytes: no sharing (same result up to the fp32 summation order). Two
+ *   calls that overlap on the GPU must not share a workspace.
+ *
+ * atom_kv4_attention_weights: sums fp32 [batch][heads][width]:
+ *     sums[b][h][t] = prev[b][h][t] + sum over sequence b's new tokens and the
+ *                     query heads of h of exp(s[t] - lse)       for t < kv_len
+ *   with q, lse, causal and scale as given to and returned by
+ *   atom_kv4_attention; a row with lse = -infinity adds nothing. prev fp32
+ *   [batch][heads][width] (may be sums itself), or NULL: 0. Elements t >= kv_len
+ *   are left as they are. kv_len > width sets the device status, like the
+ *   contradictions above. No atomics: the result is the same every time.
+ *
+ * atom_kv4_evict: per sequence and KV head, new_len = min(kv_len, budget)
+ *   tokens stay: the last min(recent, new_len), and of the others those with the
+ *   largest weights (fp32 [batch][heads][width]; equal weights: the earlier
+ *   token; NaN is smaller than everything). In their order they move to
+ *   positions 0 .. new_len - 1 of `dst` (pages to_table int32
+ *   [batch][to_table_stride], to_max_pages used). dst may be the source itself
+ *   with the same pages: the eviction is then in place; otherwise no vector of
+ *   dst may be one that is read. Written are
+ *     new_lens     int32 [batch]: new_len; must not be batch->kv_lens.
+ *     kept         int32 [batch][heads][budget]: the positions that stayed, then -1.
+ *     new_weights  fp32 [batch][heads][new_width] or NULL: their weights (may be
+ *                  `weights`, with the same width); elements >= new_len are left.
+ *   cu_q and max_q are not read. budget >= 1, 0 <= recent <= budget,
+ *   new_width >= budget.
+ *
+ * Every entry: rows, batch 0: no-op. Sizes above 2^31 - 1, a page_size < 1,
+ * q_heads not a multiple of heads: ATOM_ERR_SHAPE. Inputs must be finite where
+ * they are read; slots behind a sequence's last token may hold anything.
+ */
+typedef struct atom_kv4_cache {
+    uint8_t *k4;
+    float *ks;
+    uint8_t *v4;
+    float *vs;
+    int64_t pages, page_size, heads;
+    int64_t page_stride, token_stride, head_stride;
+} atom_kv4_cache_t;
+
+typedef struct atom_kv4_batch {
+    const int32_t *block_table;
+    int64_t table_stride, max_pages;
+    const int32_t *kv_lens;
+    const int32_t *cu_q;
+    int64_t batch, max_q;
+} atom_kv4_batch_t;
+
+ATOM_API atom_status_t atom_kv4_append(const void *k, int64_t k_token, int64_t k_head,
+                                       const void *v, int64_t v_token, int64_t v_head,
+                                       int64_t rows, const atom_kv4_cache_t *cache,
+                                       const atom_kv4_batch_t *batch, atom_stream_t stream);
+ATOM_API atom_status_t atom_kv4_gather(const atom_kv4_cache_t *cache,
+                                       const atom_kv4_batch_t *batch, int64_t rows, void *k_out,
+                                       void *v_out, atom_stream_t stream);
+ATOM_API size_t atom_kv4_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads,
+                                                   int64_t max_q);
+ATOM_API atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
+                                          int64_t rows, int64_t q_heads,
+                                          const atom_kv4_cache_t *cache,
+                                          const atom_kv4_batch_t *batch, int32_t causal,
+                                          float scale, void *out, float *lse, void *workspace,
+                                          size_t workspace_bytes, atom_stream_t stream);
+ATOM_API atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t q_head,
+                                                  int64_t rows, int64_t q_heads, const float *lse,
+                                                  const atom_kv4_cache_t *cache,
+                                                  const atom_kv4_batch_t *batch, int32_t causal,
+                                                  float scale, const float *prev, float *sums,
+                                                  int64_t width, atom_stream_t stream);
+ATOM_API atom_status_t atom_kv4_evict(const float *weights, int64_t width,
+                                      const atom_kv4_cache_t *cache,
+                                      const atom_kv4_batch_t *batch, int64_t budget,
+                                      int64_t recent, const atom_kv4_cache_t *dst,
+                                      const int32_t *to_table, int64_t to_table_stride,
+                                      int64_t to_max_pages, int32_t *new_lens, int32_t *kept,
+                                      float *new_weights, int64_t new_width,
+                                      atom_stream_t stream);
+
+/*
  * atom_probe_mma_i8 -- a measurement aid (the pages have no counterpart): the
  * dense INT8 tensor-core rate of this GPU, the second roofline denominator of
  * the W4A4 GEMM. Every CTA pair the GPU holds at once (one CTA per SM) issues

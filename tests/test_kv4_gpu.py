@@ -1,0 +1,360 @@
+"""The paged INT4 KV cache on the GPU (atom_kv4_append, atom_kv4_gather, atom_kv4_attention,
+atom_kv4_attention_weights, atom_kv4_evict) against oracle/kv4_oracle.py: writing, reading and
+evicting bit for bit, attention and its weights within the bounds that the oracle derives."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4_oracle as ko
+from w4a4_mixed_precision_b200 import atom
+
+from kv4_util import Call, assert_within, dev, host, starts
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 128 ** -0.5
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    atom.atom_device_status(clear=True)
+    yield
+    assert atom.atom_device_status(clear=True) == 0
+
+
+def check_attention(c, causal=True, scale=SCALE, **kw):
+    out, lse = atom.atom_kv4_attention(dev(c.q), c.device_cache(), c.device_batch(), causal=causal,
+                                       scale=scale, **kw)
+    want = ko.attention(c.q, c.cache, *c.sequences(), causal, scale)
+    n = c.cu_q[-1]
+    assert_within(host(out)[:n], want[0][:n], want[1][:n], "out")
+    assert_within(host(lse)[:n], want[2][:n], want[3][:n], "lse")
+    return out, lse
+
+
+# ------------------------------------------------------------------------------ append, gather
+
+@pytest.mark.parametrize("new,lens,heads,page,token_major", [
+    ([1], [1], 1, 16, False),
+    ([1, 1, 1], [1, 17, 33], 2, 16, True),
+    ([5, 0, 7, 1], [5, 9, 31, 1], 3, 7, False),
+    ([40, 3], [100, 3], 8, 24, True),
+    ([33], [33], 2, 1, False),
+    ([300, 1, 0, 129], [300, 4, 0, 500], 4, 64, False),
+])
+def test_append_and_gather_bit_exact(new, lens, heads, page, token_major):
+    c = Call(3, new, lens, heads=heads, q_heads=heads, page=page, token_major=token_major,
+             garbage=2.0)
+    cache, batch = c.device_cache(), c.device_batch()
+    atom.atom_kv4_append(dev(c.k), dev(c.v), cache, batch)
+    want = [a.copy() for a in c.cache]
+    ko.append(c.k, c.v, want, *c.sequences())
+    for got, ref in zip((cache.k4, cache.ks, cache.v4, cache.vs), want):
+        assert np.array_equal(host(got), ref)      # untouched slots included
+    k, v = atom.atom_kv4_gather(cache, batch, c.rows)
+    for got, ref in zip((k, v), ko.gather(want, *c.sequences(), c.rows)):
+        assert np.array_equal(host(got).view(np.uint16), ref.view(np.uint16))
+
+
+def test_append_takes_slices_of_a_fused_projection():
+    c = Call(5, [3, 9], [10, 9], heads=2, page=8)
+    fused = dev(np.concatenate([c.q, c.k, c.v], 1))      # [rows, 8 + 2 + 2, 128]
+    cache, batch = c.device_cache(), c.device_batch()
+    atom.atom_kv4_append(fused[:, 8:10], fused[:, 10:], cache, batch)
+    want = [a.copy() for a in c.cache]
+    ko.append(c.k, c.v, want, *c.sequences())
+    for got, ref in zip((cache.k4, cache.ks, cache.v4, cache.vs), want):
+        assert np.array_equal(host(got), ref, equal_nan=got.dtype == torch.float32)
+
+
+def test_rows_behind_the_last_sequence_are_left():
+    c = Call(6, [2, 3], [20, 3], heads=2, page=8, pad_rows=4)
+    cache, batch = c.device_cache(), c.device_batch()
+    k = torch.full((c.rows, 2, 128), 7.0, dtype=torch.float16, device="cuda")
+    v, out = k.clone(), torch.full((c.rows, 8, 128), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((c.rows, 8), 7.0, device="cuda")
+    atom.atom_kv4_gather(cache, batch, c.rows, k=k, v=v)
+    atom.atom_kv4_attention(dev(c.q), cache, batch, out=out, lse=lse)
+    for t in (k, v, out, lse):
+        assert bool((t[5:] == 7).all()) and not bool((t[:5] == 7).all())
+
+
+# ------------------------------------------------------------------------------ attention
+
+LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 1000]
+
+
+@pytest.mark.parametrize("page", [1, 16, 24, 100])
+@pytest.mark.parametrize("q_heads,heads", [(1, 1), (4, 4), (8, 1), (14, 2)])
+def test_single_tokens_of_all_lengths(page, q_heads, heads):
+    check_attention(Call(11, [1] * len(LENGTHS), LENGTHS, q_heads=q_heads, heads=heads, page=page,
+                         q_size=0.05))
+
+
+@pytest.mark.parametrize("token_major", [False, True])
+def test_empty_sequences_and_rows(token_major):
+    """Sequences with nothing cached, without new tokens, and causal rows before the cache's
+    first token: zeros and -infinity."""
+    c = Call(12, [1, 0, 4, 1, 6, 0], [0, 5, 2, 40, 0, 0], page=8, token_major=token_major,
+             q_size=0.05)
+    out, lse = check_attention(c)
+    assert bool((out[0] == 0).all()) and bool((lse[0] == -torch.inf).all())
+    assert bool((out[1:3] == 0).all()) and bool((lse[1:3] == -torch.inf).all())
+    assert bool((lse[3:6] > -torch.inf).all())
+    check_attention(c, causal=False)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,lens,q_heads,heads", [
+    ([2, 5, 8], [100, 5, 300], 8, 8),
+    ([3, 4, 1, 5], [200, 4, 77, 130], 6, 2),
+    ([5] * 4, [128, 129, 640, 31], 16, 4),
+    ([16, 17, 33], [16, 100, 700], 8, 8),
+    ([7, 100, 64], [7, 333, 64], 14, 2),
+    ([130, 1, 257], [400, 900, 257], 4, 2),
+    ([300], [300], 8, 1),
+])
+def test_several_queries(new, lens, q_heads, heads, causal):
+    check_attention(Call(13, new, lens, q_heads=q_heads, heads=heads, page=24, q_size=0.05),
+                    causal=causal)
+
+
+@pytest.mark.parametrize("heads,lens", [(1, [20000]), (2, [9001, 30, 12345]), (8, [4096] * 3)])
+def test_long_sequences_shared_between_ctas(heads, lens):
+    check_attention(Call(14, [1] * len(lens), lens, q_heads=4 * heads, heads=heads, page=64,
+                         q_size=0.05))
+
+
+def test_without_a_workspace_and_with_a_kept_one():
+    c = Call(15, [1, 3, 1], [700, 50, 3000], page=32, q_size=0.05)
+    out, lse = check_attention(c, split=False)
+    n = atom.atom_kv4_attention_workspace_bytes(c.rows, c.q_heads, c.heads, 3)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # contents do not matter
+    first = check_attention(c, workspace=ws)
+    again = check_attention(c, workspace=ws)
+    short = check_attention(c, workspace=ws[:n - 16])              # too small: not shared
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+    for a, b in zip((out, lse), short):
+        assert torch.equal(a, b)
+
+
+def test_many_short_sequences():
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 90, 3000)
+    check_attention(Call(16, [1] * 3000, lens, q_heads=2, heads=1, page=16, q_size=0.05))
+
+
+def test_strided_queries_and_sharp_scores():
+    """Queries as a slice of a projection, scores of some hundreds (one token takes all)."""
+    c = Call(17, [2, 1, 3], [90, 260, 3], q_heads=4, heads=2, page=16, q_size=3.0)
+    wide = dev(np.concatenate([c.q, c.k, c.v], 1))
+    out, lse = atom.atom_kv4_attention(wide[:, :4], c.device_cache(), c.device_batch(), scale=SCALE)
+    want = ko.attention(c.q, c.cache, *c.sequences(), True, SCALE)
+    assert_within(host(out), want[0], want[1], "out")
+    assert_within(host(lse), want[2], want[3], "lse")
+
+
+@pytest.mark.parametrize("power", [-20, 13])
+def test_values_of_any_size(power):
+    """Value scales from fp16's smallest to its largest vectors."""
+    c = Call(18, [1, 2], [400, 300], page=16, q_size=0.05)
+    c.cache[3] = (c.cache[3] * np.float32(2.0 ** power) / np.nanmax(c.cache[3])).astype(np.float32)
+    check_attention(c)
+
+
+def test_scale_and_larger_bound_on_new_tokens():
+    c = Call(19, [1, 2], [40, 50], page=16, q_size=0.05)
+    check_attention(c, scale=0.3)
+    cache = c.device_cache()
+    a = atom.atom_kv4_attention(dev(c.q), cache, c.device_batch(max_q=None))
+    want = ko.attention(c.q, c.cache, *c.sequences(), True, SCALE)
+    assert_within(host(a[0]), want[0], want[1], "out")
+
+
+# ------------------------------------------------------------------------------ weights
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,lens,q_heads,heads,page", [
+    ([1], [1], 1, 1, 16),
+    ([1, 1, 1, 1], [17, 128, 129, 1000], 8, 2, 24),
+    ([5, 0, 3], [300, 20, 3], 6, 2, 16),
+    ([64, 100], [64, 500], 4, 4, 7),
+    ([200], [200], 16, 2, 64),
+    ([1, 4], [0, 2], 4, 2, 16),
+])
+def test_attention_weights(new, lens, q_heads, heads, page, causal):
+    c = Call(21, new, lens, q_heads=q_heads, heads=heads, page=page, q_size=0.05)
+    cache, batch = c.device_cache(), c.device_batch()
+    _, lse = atom.atom_kv4_attention(dev(c.q), cache, batch, causal=causal)
+    width = max(lens) + 3
+    shape = (len(new), heads, width)
+    sums = torch.full(shape, 7.0, device="cuda")
+    atom.atom_kv4_attention_weights(dev(c.q), lse, cache, batch, sums, causal=causal)
+    want, tol = ko.attention_weights(c.q, host(lse), c.cache, *c.sequences(), causal, SCALE, width)
+    inside = np.arange(width)[None, None] < c.lens[:, None, None]
+    inside = np.broadcast_to(inside, shape)
+    got = host(sums).copy()
+    assert_within(got[inside], want[inside], tol[inside], "sums")
+    assert (got[~inside] == 7).all()
+    # added to what was there, in place
+    again = sums.clone()
+    atom.atom_kv4_attention_weights(dev(c.q), lse, cache, batch, again, prev=again, causal=causal)
+    twice = host(sums) + got
+    assert np.array_equal(host(again)[inside], twice[inside])
+    assert (host(again)[~inside] == 7).all()
+
+
+# ------------------------------------------------------------------------------ eviction
+
+@pytest.mark.parametrize("lens,budget,recent,page,to_page,token_major", [
+    ([1], 1, 0, 16, 16, False),
+    ([5, 100, 64, 0], 64, 16, 16, 24, True),
+    ([513, 1000], 100, 100, 24, 16, False),
+    ([700, 701], 512, 0, 16, 1, False),
+    ([2000, 3], 1999, 1, 100, 64, True),
+    ([1500], 1, 1, 64, 64, False),
+])
+def test_evict_matches_the_oracle(lens, budget, recent, page, to_page, token_major):
+    heads = 3
+    c = Call(31, [0] * len(lens), lens, q_heads=heads, heads=heads, page=page,
+             token_major=token_major)
+    rng = np.random.default_rng(9)
+    width = max(lens) + 2
+    w = rng.random((len(lens), heads, width)).astype(np.float32)
+    w[rng.random(w.shape) < 0.4] = 0.0           # ties
+    w[rng.random(w.shape) < 0.1] = -0.0
+    w[rng.random(w.shape) < 0.05] = np.nan
+    w[rng.random(w.shape) < 0.05] = np.inf
+    w[rng.random(w.shape) < 0.05] = -3.0
+    kept_ref, lens_ref = ko.evict(w, c.lens, budget, recent)
+    to = Call(32, [0] * len(lens), lens_ref, q_heads=heads, heads=heads, page=to_page,
+              token_major=not token_major)
+    cache, dst = c.device_cache(), to.device_cache()
+    new_lens = torch.full((len(lens),), -1, dtype=torch.int32, device="cuda")
+    kept, new_w = atom.atom_kv4_evict(dev(w), cache, c.device_batch(), budget, recent, dst,
+                                      dev(to.table), new_lens)
+    assert np.array_equal(host(new_lens), lens_ref)
+    assert np.array_equal(host(kept), kept_ref)
+    check_moved(c, w, kept_ref, lens_ref, (dst.k4, dst.ks, dst.v4, dst.vs), to.table, to_page,
+                host(new_w))
+    # in place: the same pages, the weights too
+    new_lens.fill_(-1)
+    wd = dev(w)
+    kept, new_w = atom.atom_kv4_evict(wd, cache, c.device_batch(), budget, recent, cache,
+                                      dev(c.table), new_lens, new_weights=wd if width >= budget
+                                      else None)
+    assert np.array_equal(host(new_lens), lens_ref)
+    assert np.array_equal(host(kept), kept_ref)
+    check_moved(c, w, kept_ref, lens_ref, (cache.k4, cache.ks, cache.v4, cache.vs), c.table, page,
+                host(new_w))
+
+
+def check_moved(c, w, kept, lens, got, table, page, new_w):
+    got = [host(x) for x in got]
+    for b, n in enumerate(lens):
+        to = np.arange(n)
+        for h in range(c.heads):
+            at = kept[b, h, :n]
+            for ref, x in zip(c.cache, got):
+                src = ref[c.table[b, at // c.page], at % c.page, h]
+                assert np.array_equal(x[table[b, to // page], to % page, h], src)
+            assert np.array_equal(new_w[b, h, :n], w[b, h, at], equal_nan=True)
+
+
+# ------------------------------------------------------------------------------ together
+
+def test_a_served_sequence_from_prompt_to_eviction():
+    """Prompts appended and attended, their weights summed, the cache cut in place to a budget,
+    two more tokens decoded on what is left: every step against the oracle's."""
+    heads, q_heads, page, budget, recent = 2, 8, 16, 48, 12
+    new = np.array([70, 20, 133], np.int32)
+    c = Call(41, new, new, q_heads=q_heads, heads=heads, page=page, spare_pages=6, q_size=0.05)
+    table = np.full((3, c.table.shape[1] + 1), -1, np.int32)
+    table[:, :-1] = c.table
+    free = np.setdiff1d(np.arange(c.cache[0].shape[0]), c.table)
+    table[1, 2] = free[0]                      # sequence 1 grows into a page of its own
+    cache = c.device_cache()
+    ref = [a.copy() for a in c.cache]
+    lens, table_d = dev(new.copy()), dev(table)
+    batch = atom.KV4Batch(table_d, lens, dev(c.cu_q), max_q=int(new.max()))
+    atom.atom_kv4_append(dev(c.k), dev(c.v), cache, batch)
+    ko.append(c.k, c.v, ref, table, new, c.cu_q)
+    out, lse = atom.atom_kv4_attention(dev(c.q), cache, batch)
+    want = ko.attention(c.q, ref, table, new, c.cu_q, True, SCALE)
+    assert_within(host(out), want[0], want[1], "prompt")
+    width = 160
+    sums = torch.zeros((3, heads, width), device="cuda")
+    atom.atom_kv4_attention_weights(dev(c.q), lse, cache, batch, sums, prev=sums)
+    w_ref, w_tol = ko.attention_weights(c.q, host(lse), ref, table, new, c.cu_q, True, SCALE, width)
+    assert_within(host(sums), w_ref, w_tol, "sums")
+    # evict by the sums that the library made
+    w = host(sums).copy()
+    kept_ref, lens_ref = ko.evict(w, new, budget, recent)
+    new_lens = torch.empty_like(lens)
+    kept, _ = atom.atom_kv4_evict(sums, cache, batch, budget, recent, cache, table_d, new_lens,
+                                  new_weights=sums)
+    assert np.array_equal(host(kept), kept_ref)
+    lens.copy_(new_lens)
+    moved = [a.copy() for a in ref]
+    for b, n in enumerate(lens_ref):
+        to = np.arange(n)
+        for h in range(heads):
+            at = kept_ref[b, h, :n]
+            for dst, src in zip(moved, ref):
+                dst[table[b, to // page], to % page, h] = src[table[b, at // page], at % page, h]
+    rng = np.random.default_rng(3)
+    one = atom.KV4Batch(table_d, lens, dev(starts([1, 1, 1])), max_q=1)
+    for step in range(2):
+        lens += 1
+        lens_ref = lens_ref + 1
+        q = (rng.standard_normal((3, q_heads, 128)) * 0.05).astype(np.float16)
+        kv = rng.standard_normal((2, 3, heads, 128)).astype(np.float16)
+        atom.atom_kv4_append(dev(kv[0]), dev(kv[1]), cache, one)
+        ko.append(kv[0], kv[1], moved, table, lens_ref, starts([1, 1, 1]))
+        out, lse = atom.atom_kv4_attention(dev(q), cache, one)
+        want = ko.attention(q, moved, table, lens_ref, starts([1, 1, 1]), True, SCALE)
+        assert_within(host(out), want[0], want[1], f"decode {step}")
+        assert_within(host(lse), want[2], want[3], f"decode {step}")
+
+
+# ------------------------------------------------------------------------------ streams, graphs
+
+def test_side_stream_and_captured_graph():
+    """A step captured into a graph and replayed on new values and lengths (device memory that
+    the program updates) gives what the calls give."""
+    c = Call(51, [1, 1, 1], [30, 300, 64], page=16, q_size=0.05, spare_pages=8, garbage=1.0)
+    table = np.concatenate([c.table, np.full((3, 1), 0, np.int32)], 1)
+    cache, lens = c.device_cache(), dev(c.lens)
+    batch = atom.KV4Batch(dev(table), lens, dev(c.cu_q), max_q=1)
+    q, k, v = dev(c.q), dev(c.k), dev(c.v)
+    sums = torch.zeros((3, 2, 400), device="cuda")
+
+    def step():
+        atom.atom_kv4_append(k, v, cache, batch)
+        out, lse = atom.atom_kv4_attention(q, cache, batch)
+        atom.atom_kv4_attention_weights(q, lse, cache, batch, sums)
+        return out, lse
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step()
+    rng = np.random.default_rng(2)
+    for lens_now in ([30, 300, 64], [12, 301, 1], [31, 32, 33]):
+        q.copy_(dev((rng.standard_normal(c.q.shape) * 0.05).astype(np.float16)))
+        lens.copy_(dev(np.array(lens_now, np.int32)))
+        graph.replay()
+        got = [t.clone() for t in (out, lse, sums)]
+        want = step()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(got[2], sums)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    a = atom.atom_kv4_attention(q, cache, batch, stream=other)
+    other.synchronize()
+    assert torch.equal(a[0], want[0])

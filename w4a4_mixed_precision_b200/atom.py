@@ -74,6 +74,19 @@ SIGNATURES = {
     "atom_kv_quant": ([ct.c_void_p, ct.c_int64, ct.c_void_p, ct.c_void_p, ct.c_void_p], ct.c_int),
     "atom_kv_dequant": ([ct.c_void_p, ct.c_void_p, ct.c_int64, ct.c_void_p, ct.c_void_p],
                         ct.c_int),
+    "atom_kv4_append": ([ct.c_void_p, ct.c_int64, ct.c_int64] * 2 + [ct.c_int64] +
+                        [ct.c_void_p] * 3, ct.c_int),
+    "atom_kv4_gather": ([ct.c_void_p] * 2 + [ct.c_int64] + [ct.c_void_p] * 3, ct.c_int),
+    "atom_kv4_attention_workspace_bytes": ([ct.c_int64] * 4, ct.c_size_t),
+    "atom_kv4_attention": ([ct.c_void_p] + [ct.c_int64] * 4 + [ct.c_void_p] * 2 +
+                           [ct.c_int32, ct.c_float] + [ct.c_void_p] * 3 +
+                           [ct.c_size_t, ct.c_void_p], ct.c_int),
+    "atom_kv4_attention_weights": ([ct.c_void_p] + [ct.c_int64] * 4 + [ct.c_void_p] * 3 +
+                                   [ct.c_int32, ct.c_float] + [ct.c_void_p] * 2 +
+                                   [ct.c_int64, ct.c_void_p], ct.c_int),
+    "atom_kv4_evict": ([ct.c_void_p, ct.c_int64] + [ct.c_void_p] * 2 + [ct.c_int64] * 2 +
+                       [ct.c_void_p] * 2 + [ct.c_int64] * 2 + [ct.c_void_p] * 3 +
+                       [ct.c_int64, ct.c_void_p], ct.c_int),
     "atom_debug_wait_timeout": ([ct.c_uint64, ct.c_void_p], ct.c_int),
     "atom_probe_mma_i8": ([ct.c_int64, ct.POINTER(ct.c_int32), ct.c_void_p], ct.c_int),
     "atom_device_status": ([ct.c_int], ct.c_int),
@@ -495,6 +508,312 @@ def atom_kv_dequant(q4: torch.Tensor, scales: torch.Tensor, out: Optional[torch.
                                groups, _dev(out, torch.float16, "out"), _stream(stream))
     _check("atom_kv_dequant", st)
     return out
+
+
+class _CacheStruct(ct.Structure):
+    _fields_ = ([(n, ct.c_void_p) for n in ("k4", "ks", "v4", "vs")] +
+                [(n, ct.c_int64) for n in ("pages", "page_size", "heads", "page_stride",
+                                           "token_stride", "head_stride")])
+
+
+class _BatchStruct(ct.Structure):
+    _fields_ = [("block_table", ct.c_void_p), ("table_stride", ct.c_int64),
+                ("max_pages", ct.c_int64), ("kv_lens", ct.c_void_p), ("cu_q", ct.c_void_p),
+                ("batch", ct.c_int64), ("max_q", ct.c_int64)]
+
+
+def _kv4_check(t: torch.Tensor, dtype: torch.dtype, name: str, device=None) -> torch.Tensor:
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
+def _kv4_rows(t: torch.Tensor, heads: Optional[int], name: str, device):
+    """Pointer, token stride and head stride of fp16 [rows, heads, 128]; a dimension of
+    one has no stride of its own."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must have shape (rows, {heads or 'heads'}, 128), got "
+                         f"{tuple(shape)}")
+    _kv4_check(t, torch.float16, name, device)
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
+
+
+def _kv4_contiguous(t: torch.Tensor, dtype: torch.dtype, shape, name: str, device) -> int:
+    _expect_shape(t, shape, name)
+    _kv4_check(t, dtype, name, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class KV4Cache:
+    """A paged INT4 KV cache (see include/atom.h): codes k4, v4 uint8 [pages, page_size,
+    heads, 64] and scales ks, vs float32 [pages, page_size, heads], all on one device, in
+    any layout that keeps a vector's 64 bytes together and is the same for the four (views
+    of [pages, heads, page_size, ...] storage, for example). The object holds the tensors'
+    addresses: their storage must stay in place."""
+
+    def __init__(self, k4: torch.Tensor, ks: torch.Tensor, v4: torch.Tensor, vs: torch.Tensor):
+        if k4.dim() != 4 or k4.shape[3] != 64:
+            raise ValueError(f"k4 must have shape (pages, page_size, heads, 64), got "
+                             f"{tuple(k4.shape)}")
+        lead = tuple(k4.shape[:3])
+        _expect_shape(v4, lead + (64,), "v4")
+        _expect_shape(ks, lead, "ks")
+        _expect_shape(vs, lead, "vs")
+        real = [i for i in range(3) if lead[i] > 1]   # dimensions whose stride counts
+        for t, unit, name in ((k4, 64, "k4"), (v4, 64, "v4"), (vs, 1, "vs")):
+            if any(t.stride(i) != unit * ks.stride(i) for i in real) or (
+                    unit == 64 and t.stride(3) != 1):
+                raise ValueError(f"{name} must have the layout of ks (strides, in vectors)")
+        device = k4.device
+        for t, dtype, name in ((k4, torch.uint8, "k4"), (ks, torch.float32, "ks"),
+                               (v4, torch.uint8, "v4"), (vs, torch.float32, "vs")):
+            _kv4_check(t, dtype, name, device)
+        self.k4, self.ks, self.v4, self.vs = k4, ks, v4, vs
+        self.pages, self.page_size, self.heads = lead
+        self.device = device
+        strides = [ks.stride(i) if i in real else 0 for i in range(3)]
+        self.struct = _CacheStruct(k4.data_ptr(), ks.data_ptr(), v4.data_ptr(), vs.data_ptr(),
+                                   *lead, *strides)
+        self._ref = ct.addressof(self.struct)
+
+
+def empty_kv4_cache(pages: int, page_size: int, heads: int, device,
+                    token_major: bool = False) -> KV4Cache:
+    """A KV4Cache in new storage: [pages, heads, page_size, ...] (a head's tokens of a page
+    together) or, token_major, [pages, page_size, heads, ...] (atom_kv_quant's order). Its
+    contents are undefined."""
+    lead = (pages, page_size, heads) if token_major else (pages, heads, page_size)
+    parts = []
+    for _ in range(2):
+        q4 = torch.empty(lead + (64,), dtype=torch.uint8, device=device)
+        scales = torch.empty(lead, dtype=torch.float32, device=device)
+        parts += [q4, scales] if token_major else [q4.transpose(1, 2), scales.transpose(1, 2)]
+    return KV4Cache(*parts)
+
+
+class KV4Batch:
+    """The sequences of a call on a KV4Cache (see include/atom.h): block_table int32 [batch,
+    max_pages] (a row's entries together), kv_lens int32 [batch] (the new tokens included)
+    and cu_q int32 [batch + 1], on one device; max_q bounds the new tokens of a sequence
+    (default: no bound but the call's rows). The object holds the tensors' addresses: a
+    program updates their values in place from step to step."""
+
+    def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor,
+                 max_q: Optional[int] = None):
+        if kv_lens.dim() != 1:
+            raise ValueError(f"kv_lens must have shape (batch,), got {tuple(kv_lens.shape)}")
+        batch = kv_lens.shape[0]
+        if block_table.dim() != 2 or block_table.shape[0] != batch:
+            raise ValueError(f"block_table must have shape ({batch}, max_pages), got "
+                             f"{tuple(block_table.shape)}")
+        _expect_shape(cu_q, (batch + 1,), "cu_q")
+        if max_q is not None and max_q < 0:
+            raise ValueError("max_q must not be negative")
+        self.device = kv_lens.device
+        for t, name in ((block_table, "block_table"), (kv_lens, "kv_lens"), (cu_q, "cu_q")):
+            _kv4_check(t, torch.int32, name, self.device)
+        width = block_table.shape[1]
+        if (block_table.stride(1) != 1 and width > 1) or not kv_lens.is_contiguous() or (
+                not cu_q.is_contiguous()):
+            raise ValueError("block_table rows, kv_lens and cu_q must be contiguous")
+        self.block_table, self.kv_lens, self.cu_q = block_table, kv_lens, cu_q
+        self.batch = batch
+        self.max_q = 2 ** 31 - 1 if max_q is None else max_q
+        stride = block_table.stride(0) if batch > 1 else width
+        self.struct = _BatchStruct(block_table.data_ptr(), stride, width, kv_lens.data_ptr(),
+                                   cu_q.data_ptr(), batch, self.max_q)
+        self._ref = ct.addressof(self.struct)
+
+
+class _kv4_call:
+    """Runs a call on `device`: makes it the current device, and the call's stream (default:
+    the device's current one) the one whose memory new tensors come from."""
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self.contexts = device, stream, ()
+
+    def __enter__(self) -> int:
+        if self.stream is None and torch.cuda.current_device() == self.device.index:
+            return torch.cuda.current_stream().cuda_stream
+        if self.stream is None:
+            self.contexts = (torch.cuda.device(self.device),)
+        else:
+            given = self.stream
+            if not hasattr(given, "cuda_stream"):
+                given = torch.cuda.ExternalStream(int(given), device=self.device)
+            if given.device != self.device:
+                raise ValueError(f"the stream is on {given.device}, the tensors on {self.device}")
+            self.contexts = (torch.cuda.device(self.device), torch.cuda.stream(given))
+        for c in self.contexts:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _kv4_same_device(cache: KV4Cache, batch: KV4Batch) -> torch.device:
+    if batch.device != cache.device:
+        raise ValueError(f"the batch must be on {cache.device}, got {batch.device}")
+    return cache.device
+
+
+def atom_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, batch: KV4Batch,
+                    stream=None) -> None:
+    """Quantizes new keys and values, fp16 [rows, heads, 128] (strided views are taken),
+    into their slots of the cache: the last positions of their sequences."""
+    device = _kv4_same_device(cache, batch)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    kp, vp = _kv4_rows(k, cache.heads, "k", device), _kv4_rows(v, cache.heads, "v", device)
+    with _kv4_call(device, stream) as s:
+        st = lib().atom_kv4_append(*kp, *vp, k.shape[0], cache._ref, batch._ref, s)
+    _check("atom_kv4_append", st)
+
+
+def atom_kv4_gather(cache: KV4Cache, batch: KV4Batch, rows: int,
+                    k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Reads the tokens that atom_kv4_append wrote back as fp16 (k, v), each [rows, heads,
+    128] with atom_kv_dequant's values. Rows that no sequence has are not written."""
+    device = _kv4_same_device(cache, batch)
+    shape = (rows, cache.heads, 128)
+    with _kv4_call(device, stream) as s:
+        if k is None:
+            k = torch.empty(shape, dtype=torch.float16, device=device)
+        if v is None:
+            v = torch.empty(shape, dtype=torch.float16, device=device)
+        st = lib().atom_kv4_gather(cache._ref, batch._ref, rows,
+                                   _kv4_contiguous(k, torch.float16, shape, "k", device),
+                                   _kv4_contiguous(v, torch.float16, shape, "v", device), s)
+    _check("atom_kv4_gather", st)
+    return k, v
+
+
+def atom_kv4_attention_workspace_bytes(rows: int, q_heads: int, heads: int, max_q: int) -> int:
+    return int(lib().atom_kv4_attention_workspace_bytes(rows, q_heads, heads, max_q))
+
+
+def atom_kv4_attention(q: torch.Tensor, cache: KV4Cache, batch: KV4Batch, causal: bool = True,
+                       scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, split: bool = True,
+                       stream=None):
+    """Attention of new tokens over the INT4 cache (their own keys and values already
+    appended): q fp16 [rows, q_heads, 128] (strided views are taken) -> (out fp16 [rows,
+    q_heads, 128], lse float32 [rows, q_heads]). `scale` defaults to 1/sqrt(128).
+
+    `workspace` (uint8) is the scratch with which a sequence's cached tokens are shared
+    between CTAs; when it is None and `split` is true, one of
+    atom_kv4_attention_workspace_bytes() bytes is allocated here."""
+    device = _kv4_same_device(cache, batch)
+    qp = _kv4_rows(q, None, "q", device)
+    rows, q_heads = q.shape[0], q.shape[1]
+    with _kv4_call(device, stream) as s:
+        if out is None:
+            out = torch.empty((rows, q_heads, 128), dtype=torch.float16, device=device)
+        if lse is None:
+            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=device)
+        ws_ptr, ws_bytes = None, 0
+        if split:
+            if workspace is None:
+                ws_bytes = lib().atom_kv4_attention_workspace_bytes(rows, q_heads, cache.heads,
+                                                                    batch.max_q)
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+            else:
+                _kv4_check(workspace, torch.uint8, "workspace", device)
+                if not workspace.is_contiguous():
+                    raise ValueError("workspace must be contiguous")
+                ws_bytes = workspace.numel()
+            ws_ptr = workspace.data_ptr() if ws_bytes else None
+        st = lib().atom_kv4_attention(
+            *qp, rows, q_heads, cache._ref, batch._ref, 1 if causal else 0,
+            128.0 ** -0.5 if scale is None else scale,
+            _kv4_contiguous(out, torch.float16, (rows, q_heads, 128), "out", device),
+            _kv4_contiguous(lse, torch.float32, (rows, q_heads), "lse", device),
+            ws_ptr, ws_bytes, s)
+    _check("atom_kv4_attention", st)
+    return out, lse
+
+
+def atom_kv4_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: KV4Cache,
+                               batch: KV4Batch, sums: torch.Tensor,
+                               prev: Optional[torch.Tensor] = None, causal: bool = True,
+                               scale: Optional[float] = None, stream=None) -> torch.Tensor:
+    """The attention weight that each cached token received from the call's queries, summed
+    over a KV head's query heads: float32 [batch, heads, width], written to `sums` (added to
+    `prev`, which may be `sums` itself) for the tokens of each sequence. q, causal and scale
+    as given to atom_kv4_attention, lse as it returned."""
+    device = _kv4_same_device(cache, batch)
+    qp = _kv4_rows(q, None, "q", device)
+    rows, q_heads = q.shape[0], q.shape[1]
+    if sums.dim() != 3:
+        raise ValueError("sums must have shape (batch, heads, width)")
+    width = sums.shape[2]
+    shape = (batch.batch, cache.heads, width)
+    sums_ptr = _kv4_contiguous(sums, torch.float32, shape, "sums", device)
+    prev_ptr = None
+    if prev is not None:
+        prev_ptr = _kv4_contiguous(prev, torch.float32, shape, "prev", device)
+    with _kv4_call(device, stream) as s:
+        st = lib().atom_kv4_attention_weights(
+            *qp, rows, q_heads, _kv4_contiguous(lse, torch.float32, (rows, q_heads), "lse", device),
+            cache._ref, batch._ref, 1 if causal else 0, 128.0 ** -0.5 if scale is None else scale,
+            prev_ptr, sums_ptr, width, s)
+    _check("atom_kv4_attention_weights", st)
+    return sums
+
+
+def atom_kv4_evict(weights: torch.Tensor, cache: KV4Cache, batch: KV4Batch, budget: int,
+                   recent: int, dst: KV4Cache, to_table: torch.Tensor, new_lens: torch.Tensor,
+                   kept: Optional[torch.Tensor] = None,
+                   new_weights: Optional[torch.Tensor] = None, stream=None):
+    """Keeps `budget` tokens of each sequence and KV head: the last `recent` ones and those
+    with the largest `weights` (float32 [batch, heads, width]), moved in their order to the
+    first positions of `dst` (pages to_table int32 [batch, pages]); `dst` and `to_table` may
+    be the cache and its own table. Writes new_lens int32 [batch] (not batch.kv_lens) and
+    returns (kept int32 [batch, heads, budget], new_weights float32 [batch, heads,
+    new_width]); elements of new_weights behind a sequence's new length are not written."""
+    device = _kv4_same_device(cache, batch)
+    if dst.device != device:
+        raise ValueError(f"dst must be on {device}, got {dst.device}")
+    n, heads = batch.batch, cache.heads
+    if weights.dim() != 3:
+        raise ValueError("weights must have shape (batch, heads, width)")
+    width = weights.shape[2]
+    weights_ptr = _kv4_contiguous(weights, torch.float32, (n, heads, width), "weights", device)
+    if to_table.dim() != 2 or to_table.shape[0] != n:
+        raise ValueError(f"to_table must have shape ({n}, pages), got {tuple(to_table.shape)}")
+    _kv4_check(to_table, torch.int32, "to_table", device)
+    to_pages = to_table.shape[1]
+    if to_pages > 1 and to_table.stride(1) != 1:
+        raise ValueError("to_table rows must be contiguous")
+    lens_ptr = _kv4_contiguous(new_lens, torch.int32, (n,), "new_lens", device)
+    with _kv4_call(device, stream) as s:
+        if kept is None:
+            kept = torch.empty((n, heads, budget), dtype=torch.int32, device=device)
+        if new_weights is None:
+            new_weights = torch.empty((n, heads, budget), dtype=torch.float32, device=device)
+        new_width = new_weights.shape[-1]
+        st = lib().atom_kv4_evict(
+            weights_ptr, width, cache._ref, batch._ref, budget, recent, dst._ref,
+            to_table.data_ptr(), to_table.stride(0) if n > 1 else to_pages, to_pages, lens_ptr,
+            _kv4_contiguous(kept, torch.int32, (n, heads, budget), "kept", device),
+            _kv4_contiguous(new_weights, torch.float32, (n, heads, new_width), "new_weights",
+                            device), new_width, s)
+    _check("atom_kv4_evict", st)
+    return kept, new_weights
 
 
 def atom_gemm_workspace_bytes(M: int, N: int, K: int) -> int:

@@ -12,6 +12,10 @@
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "kv.cuh"
+#include "kv4.cuh"
+#include "kv4_attn.cuh"
+#include "kv4_evict.cuh"
+#include "kv4_weights.cuh"
 #include "probe.cuh"
 #include "tiled.cuh"
 #include "w8a8.cuh"
@@ -34,6 +38,8 @@ struct DeviceState {
   bool small_attr = false;       // shared-memory limit set for the small-M GEMM kernels
   bool w8a8_attr = false;
   int w8a8_clusters = 0;          // co-resident CTA pairs of the W8A8 kernel
+  std::atomic<bool> kv4_attr[2] = {};   // by query tile (8, 16 rows): publishes kv4_ctas
+  int kv4_ctas[2] = {};           // co-resident CTAs of the cache attention kernel
   uint32_t quant_smem_set = 0;
   std::atomic<void *> noalloc_scratch{nullptr};  // device address of g_noalloc_scratch here
   std::atomic<uint32_t> quant_calls{0};   // picks each quantizer call's row-counter slot
@@ -861,6 +867,10 @@ const char *atom_status_string(atom_status_t status) {
 int atom_version(void) { return 100; }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- paged INT4 KV cache
+
+#include "kv4_api.cuh"
 
 // ---------------------------------------------------------------- allocation-free GEMM
 //

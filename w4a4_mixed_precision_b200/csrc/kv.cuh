@@ -27,6 +27,47 @@ namespace atomk {
 
 constexpr int kKvThreads = 256;
 
+// The codes of 16 elements (fp16 pairs `w`) of a group that the 8 lanes of
+// `team_mask` hold together, packed, and the group's scale.
+__device__ __forceinline__ uint2 kv_encode16(const uint32_t (&w)[8], unsigned team_mask,
+                                             float &scale) {
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(v[j]));
+  amax = fmaxf(amax, __shfl_xor_sync(team_mask, amax, 4));
+  amax = fmaxf(amax, __shfl_xor_sync(team_mask, amax, 2));
+  amax = fmaxf(amax, __shfl_xor_sync(team_mask, amax, 1));
+  float inv = 0.f;
+  scale = 0.f;
+  if (amax > 0.f) {
+    scale = __fdiv_rn(amax, 7.f);
+    inv = __fdiv_rn(7.f, amax);
+  }
+  // the low byte of fp32(1.5 * 2^23 + rint(x * inv)) is the code in two's
+  // complement; the product is rounded to fp32 before the add rounds to an
+  // integer (__fmul_rn / __fadd_rn are never contracted into an FMA)
+  uint32_t c[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) c[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));
+  uint32_t out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t ev = __byte_perm(__byte_perm(c[8 * h], c[8 * h + 2], 0x0040),
+                                    __byte_perm(c[8 * h + 4], c[8 * h + 6], 0x0040), 0x5410);
+    const uint32_t od = __byte_perm(__byte_perm(c[8 * h + 1], c[8 * h + 3], 0x0040),
+                                    __byte_perm(c[8 * h + 5], c[8 * h + 7], 0x0040), 0x5410);
+    out[h] = (ev & 0x0F0F0F0Fu) | ((od << 4) & 0xF0F0F0F0u);
+  }
+  return make_uint2(out[0], out[1]);
+}
+
 __global__ void __launch_bounds__(kKvThreads)
 kv_quant_kernel(const __half *__restrict__ x, int64_t groups, uint8_t *__restrict__ q4,
                 float *__restrict__ scales) {
@@ -38,41 +79,27 @@ kv_quant_kernel(const __half *__restrict__ x, int64_t groups, uint8_t *__restric
     const uint4 *src = reinterpret_cast<const uint4 *>(x + g * 128 + sub * 16);
     const uint4 a = __ldg(src), b = __ldg(src + 1);
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    float v[16];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-      v[2 * j] = f.x;
-      v[2 * j + 1] = f.y;
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    amax = fmaxf(amax, __shfl_xor_sync(team_mask, amax, 4));
-    amax = fmaxf(amax, __shfl_xor_sync(team_mask, amax, 2));
-    amax = fmaxf(amax, __shfl_xor_sync(team_mask, amax, 1));
-    float scale = 0.f, inv = 0.f;
-    if (amax > 0.f) {
-      scale = __fdiv_rn(amax, 7.f);
-      inv = __fdiv_rn(7.f, amax);
-    }
-    // the low byte of fp32(1.5 * 2^23 + rint(x * inv)) is the code in two's
-    // complement; the product is rounded to fp32 before the add rounds to an
-    // integer (__fmul_rn / __fadd_rn are never contracted into an FMA)
-    uint32_t c[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) c[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));
-    uint32_t out[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t ev = __byte_perm(__byte_perm(c[8 * h], c[8 * h + 2], 0x0040),
-                                      __byte_perm(c[8 * h + 4], c[8 * h + 6], 0x0040), 0x5410);
-      const uint32_t od = __byte_perm(__byte_perm(c[8 * h + 1], c[8 * h + 3], 0x0040),
-                                      __byte_perm(c[8 * h + 5], c[8 * h + 7], 0x0040), 0x5410);
-      out[h] = (ev & 0x0F0F0F0Fu) | ((od << 4) & 0xF0F0F0F0u);
-    }
-    *reinterpret_cast<uint2 *>(q4 + g * 64 + sub * 8) = make_uint2(out[0], out[1]);
+    float scale;
+    *reinterpret_cast<uint2 *>(q4 + g * 64 + sub * 8) = kv_encode16(w, team_mask, scale);
     if (sub == 0) scales[g] = scale;
+  }
+}
+
+// 16 elements (fp16 pairs) from 8 bytes of codes and the group's scale.
+__device__ __forceinline__ void kv_decode16(uint2 p, float s, uint32_t (&o)[8]) {
+  const uint32_t w[2] = {p.x, p.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // byte j: element 2j in the low nibble, 2j+1 in the high nibble. A
+    // nibble n is the code q = (n ^ 8) - 8; fp32(q) is made without a
+    // conversion instruction, as the float with bits 0x4B400000 | (n ^ 8)
+    // (= 1.5*2^23 + (n ^ 8)) minus 1.5*2^23 + 8, both steps exact. The pair
+    // of products goes to fp16 in one packed round-to-nearest conversion.
+    const uint32_t byte = w[j >> 2] >> (8 * (j & 3));
+    const float q0 = __fsub_rn(__uint_as_float(0x4B400000u | ((byte & 0xFu) ^ 8u)), 12582920.f);
+    const float q1 =
+        __fsub_rn(__uint_as_float(0x4B400000u | (((byte >> 4) & 0xFu) ^ 8u)), 12582920.f);
+    o[j] = pack_half2_rn(__fmul_rn(q0, s), __fmul_rn(q1, s));
   }
 }
 
@@ -85,21 +112,8 @@ kv_dequant_kernel(const uint8_t *__restrict__ q4, const float *__restrict__ scal
        g += stride) {
     const uint2 p = __ldg(reinterpret_cast<const uint2 *>(q4 + g * 64 + sub * 8));
     const float s = __ldg(scales + g);
-    const uint32_t w[2] = {p.x, p.y};
     uint32_t o[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // byte j: element 2j in the low nibble, 2j+1 in the high nibble. A
-      // nibble n is the code q = (n ^ 8) - 8; fp32(q) is made without a
-      // conversion instruction, as the float with bits 0x4B400000 | (n ^ 8)
-      // (= 1.5*2^23 + (n ^ 8)) minus 1.5*2^23 + 8, both steps exact. The pair
-      // of products goes to fp16 in one packed round-to-nearest conversion.
-      const uint32_t byte = w[j >> 2] >> (8 * (j & 3));
-      const float q0 = __fsub_rn(__uint_as_float(0x4B400000u | ((byte & 0xFu) ^ 8u)), 12582920.f);
-      const float q1 =
-          __fsub_rn(__uint_as_float(0x4B400000u | (((byte >> 4) & 0xFu) ^ 8u)), 12582920.f);
-      o[j] = pack_half2_rn(__fmul_rn(q0, s), __fmul_rn(q1, s));
-    }
+    kv_decode16(p, s, o);
     uint4 *dst = reinterpret_cast<uint4 *>(out + g * 128 + sub * 16);
     dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);

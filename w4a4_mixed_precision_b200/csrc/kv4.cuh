@@ -1,0 +1,95 @@
+// kv4.cuh -- the paged INT4 KV cache: writing new tokens to it (append) and
+// reading them back (gather). The encoding is kv.cuh's: one group per (token,
+// head) vector of 128 elements.
+//
+// Token `row` of the call is new token i = row - cu_q[b] of its sequence b and
+// sits at position kv_lens[b] - (cu_q[b+1] - cu_q[b]) + i, whose page is
+// table[b][position / page_size].
+//
+// Both kernels stream: 8 lanes own one vector (16 elements each), as the
+// contiguous cache kernels do. Every team finds its token's sequence by a
+// binary search of cu_q.
+#pragma once
+
+#include "kv.cuh"
+#include "kv4_plan.h"
+
+namespace atomk {
+
+struct Kv4Rows {
+  uint8_t *k4, *v4;
+  float *ks, *vs;
+  Kv4Geom geom;
+  Kv4Seqs seqs;
+  __half *k, *v;                          // append: read; gather: written
+  int64_t k_token, k_head, v_token, v_head;   // strides of k and v, in elements
+};
+
+// The last sequence that begins at `row` or before (cu_q ascending).
+__device__ __forceinline__ int kv4_sequence_of(const Kv4Seqs &s, int row) {
+  int lo = 0, hi = s.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(s.cu_q + mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Vector number of (row, head)'s slot, or -1 where there is none; what the
+// device arrays get wrong is recorded in the status word.
+__device__ __forceinline__ int64_t kv4_row_vector(const Kv4Rows &p, int row, int head) {
+  const Kv4Seqs &q = p.seqs;
+  const int b = kv4_sequence_of(q, row);
+  const int q0 = __ldg(q.cu_q + b), q1 = __ldg(q.cu_q + b + 1);
+  if (row < q0 || row >= q1) return -1;   // behind the last sequence
+  const Kv4Seq s = kv4_seq_of(q0, q1, __ldg(q.kv_lens + b), q.rows, q.capacity);
+  if (!s.ok || s.qn > s.len) {
+    report_status(1 /* ATOM_ERR_INVALID_ARG */);
+    return -1;
+  }
+  const int pos = s.len - s.qn + row - q0;
+  const int page_no = kv4_div(pos, p.geom.by_page);
+  const int page = __ldg(q.table + b * q.table_stride + page_no);
+  const int64_t vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, head);
+  if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
+  return vec;
+}
+
+template <bool kAppend>
+__global__ void __launch_bounds__(kKvThreads) kv4_rows_kernel(const Kv4Rows p) {
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const unsigned team_mask = 0xFFu << (8 * (lane >> 3));
+  const int heads = p.geom.heads;
+  const int64_t items = static_cast<int64_t>(p.seqs.rows) * heads * 2;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 3);
+  for (int64_t it = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3; it < items;
+       it += stride) {
+    const int row = static_cast<int>(it / (2 * heads));
+    const int r = static_cast<int>(it - static_cast<int64_t>(row) * (2 * heads));
+    const bool value = r >= heads;
+    const int head = value ? r - heads : r;
+    const int64_t vec = kv4_row_vector(p, row, head);
+    if (vec < 0) continue;   // the same for the team's 8 lanes
+    __half *x = (value ? p.v + row * p.v_token + head * p.v_head
+                       : p.k + row * p.k_token + head * p.k_head) + sub * 16;
+    uint8_t *q4 = (value ? p.v4 : p.k4) + vec * 64 + sub * 8;
+    float *sc = (value ? p.vs : p.ks) + vec;
+    if constexpr (kAppend) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x));
+      const uint4 b = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      float scale;
+      *reinterpret_cast<uint2 *>(q4) = kv_encode16(w, team_mask, scale);
+      if (sub == 0) *sc = scale;
+    } else {
+      uint32_t o[8];
+      kv_decode16(__ldg(reinterpret_cast<const uint2 *>(q4)), __ldg(sc), o);
+      uint4 *dst = reinterpret_cast<uint4 *>(x);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+}  // namespace atomk

@@ -1,0 +1,342 @@
+// kv4_api.cuh -- host side of the paged INT4 KV cache's entry points: argument
+// checks and launches. Part of the translation unit atom_lib.cu.
+#pragma once
+
+namespace {
+
+bool kv4_fits(int64_t v) { return v <= INT32_MAX; }
+
+// Sizes and strides, then (with `touched`) pointers.
+atom_status_t kv4_check_cache(const atom_kv4_cache_t *c, bool touched) {
+  if (!c || c->pages < 0 || c->heads < 0 || c->page_stride < 0 || c->token_stride < 0 ||
+      c->head_stride < 0)
+    return ATOM_ERR_INVALID_ARG;
+  if (c->page_size < 1 || c->heads < 1 || !kv4_fits(c->pages) || !kv4_fits(c->page_size) ||
+      !kv4_fits(c->heads))
+    return ATOM_ERR_SHAPE;
+  if (!touched) return ATOM_OK;
+  if (!c->k4 || !c->ks || !c->v4 || !c->vs) return ATOM_ERR_INVALID_ARG;
+  if (!aligned(c->k4, 16) || !aligned(c->v4, 16) || !aligned(c->ks, 4) || !aligned(c->vs, 4))
+    return ATOM_ERR_ALIGN;
+  return ATOM_OK;
+}
+
+atom_status_t kv4_check_table(const int32_t *table, int64_t stride, int64_t max_pages) {
+  if (max_pages < 0 || stride < 0) return ATOM_ERR_INVALID_ARG;
+  if (stride < max_pages) return ATOM_ERR_SHAPE;
+  if (!table && max_pages > 0) return ATOM_ERR_INVALID_ARG;
+  return aligned(table, 4) ? ATOM_OK : ATOM_ERR_ALIGN;
+}
+
+atom_status_t kv4_check_batch(const atom_kv4_batch_t *b, bool rows_read) {
+  if (!b || b->batch < 0 || b->max_q < 0) return ATOM_ERR_INVALID_ARG;
+  if (!kv4_fits(b->batch)) return ATOM_ERR_SHAPE;
+  if (b->batch == 0) return ATOM_OK;
+  const atom_status_t st = kv4_check_table(b->block_table, b->table_stride, b->max_pages);
+  if (st != ATOM_OK) return st;
+  if (!b->kv_lens || (rows_read && !b->cu_q)) return ATOM_ERR_INVALID_ARG;
+  if (!aligned(b->kv_lens, 4) || !aligned(b->cu_q, 4)) return ATOM_ERR_ALIGN;
+  return ATOM_OK;
+}
+
+// fp16 row tensors [rows][heads][128]
+atom_status_t kv4_check_rows(const void *x, int64_t token, int64_t head) {
+  if (token < 0 || head < 0) return ATOM_ERR_INVALID_ARG;
+  if (token % 8 != 0 || head % 8 != 0) return ATOM_ERR_SHAPE;
+  if (!x) return ATOM_ERR_INVALID_ARG;
+  return aligned(x, 16) ? ATOM_OK : ATOM_ERR_ALIGN;
+}
+
+atomk::Kv4Geom kv4_geom(const atom_kv4_cache_t *c) {
+  atomk::Kv4Geom g;
+  g.page_stride = c->page_stride;
+  g.token_stride = c->token_stride;
+  g.head_stride = c->head_stride;
+  g.pages = static_cast<int>(c->pages);
+  g.page_size = static_cast<int>(c->page_size);
+  g.heads = static_cast<int>(c->heads);
+  g.by_page = atomk::kv4_div_by(c->page_size);
+  return g;
+}
+
+int kv4_capacity(int64_t max_pages, int64_t page_size) {
+  return max_pages > INT32_MAX / page_size ? INT32_MAX : static_cast<int>(max_pages * page_size);
+}
+
+atomk::Kv4Seqs kv4_seqs(const atom_kv4_batch_t *b, const atom_kv4_cache_t *c, int64_t rows) {
+  atomk::Kv4Seqs s;
+  s.table = b->block_table;
+  s.table_stride = b->table_stride;
+  s.kv_lens = b->kv_lens;
+  s.cu_q = b->cu_q;
+  s.batch = static_cast<int>(b->batch);
+  s.rows = static_cast<int>(rows);
+  s.capacity = kv4_capacity(b->max_pages, c->page_size);
+  return s;
+}
+
+atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_head, const void *v,
+                       int64_t v_token, int64_t v_head, int64_t rows, const atom_kv4_cache_t *cache,
+                       const atom_kv4_batch_t *batch, atom_stream_t stream) {
+  if (rows < 0) return ATOM_ERR_INVALID_ARG;
+  if (!kv4_fits(rows)) return ATOM_ERR_SHAPE;
+  const bool touched = rows > 0 && batch != nullptr && batch->batch > 0;
+  atom_status_t st;
+  if ((st = kv4_check_cache(cache, touched)) != ATOM_OK) return st;
+  if ((st = kv4_check_batch(batch, touched)) != ATOM_OK) return st;
+  if (!touched) return ATOM_OK;
+  if ((st = kv4_check_rows(k, k_token, k_head)) != ATOM_OK) return st;
+  if ((st = kv4_check_rows(v, v_token, v_head)) != ATOM_OK) return st;
+  DeviceState *dev = nullptr;
+  if ((st = current_device(&dev)) != ATOM_OK) return st;
+  atomk::Kv4Rows p;
+  p.k4 = cache->k4;
+  p.v4 = cache->v4;
+  p.ks = cache->ks;
+  p.vs = cache->vs;
+  p.geom = kv4_geom(cache);
+  p.seqs = kv4_seqs(batch, cache, rows);
+  p.k = static_cast<__half *>(const_cast<void *>(k));
+  p.v = static_cast<__half *>(const_cast<void *>(v));
+  p.k_token = k_token;
+  p.k_head = k_head;
+  p.v_token = v_token;
+  p.v_head = v_head;
+  const int grid = kv_grid(dev, rows * cache->heads * 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (append)
+    atomk::kv4_rows_kernel<true><<<grid, atomk::kKvThreads, 0, s>>>(p);
+  else
+    atomk::kv4_rows_kernel<false><<<grid, atomk::kKvThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
+}
+
+// Query rows a CTA of the decode kernel takes at once, 8 or 16: the smallest
+// that holds every sequence's rows of a KV head, so that the cache is read once.
+int kv4_decode_nt(int64_t max_q, int64_t group) { return max_q * group <= 8 ? 1 : 2; }
+
+// CTAs of the decode kernel: all that the GPU holds at once.
+atom_status_t kv4_decode_ctas(DeviceState *dev, int nt, int *ctas) {
+  using namespace atomk::kv4_decode_cfg;
+  if (!dev->kv4_attr[nt - 1].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!dev->kv4_attr[nt - 1].load(std::memory_order_relaxed)) {
+      const void *fn = nt == 1 ? reinterpret_cast<const void *>(atomk::kv4_decode_kernel<1>)
+                               : reinterpret_cast<const void *>(atomk::kv4_decode_kernel<2>);
+      int per_sm = 0;
+      if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(smem_bytes(nt))) != cudaSuccess ||
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem_bytes(nt)) !=
+              cudaSuccess ||
+          per_sm < 1)
+        return ATOM_ERR_CUDA;
+      dev->kv4_ctas[nt - 1] = per_sm * dev->sm_count;
+      dev->kv4_attr[nt - 1].store(true, std::memory_order_release);
+    }
+  }
+  *ctas = dev->kv4_ctas[nt - 1];
+  return ATOM_OK;
+}
+
+// Launch that may overlap the end of the kernel before it in the stream (the
+// kernel waits for that one before it touches memory).
+template <class P>
+cudaError_t kv4_launch(void (*fn)(const P), int grid, int threads, size_t smem,
+                       atom_stream_t stream, const P &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+// Sizes shared by the two attention entry points.
+atom_status_t kv4_check_queries(int64_t rows, int64_t q_heads, float scale,
+                                const atom_kv4_cache_t *cache, const atom_kv4_batch_t *batch,
+                                bool *touched) {
+  if (rows < 0 || q_heads < 0) return ATOM_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.f)) return ATOM_ERR_INVALID_ARG;   // not finite
+  *touched = rows > 0 && batch != nullptr && batch->batch > 0;
+  atom_status_t st;
+  if ((st = kv4_check_cache(cache, *touched)) != ATOM_OK) return st;
+  if ((st = kv4_check_batch(batch, *touched)) != ATOM_OK) return st;
+  if (!kv4_fits(rows) || q_heads < 1 || q_heads % cache->heads != 0 || !kv4_fits(q_heads) ||
+      !kv4_fits(rows * (q_heads / cache->heads)))   // query rows of a KV head
+    return ATOM_ERR_SHAPE;
+  return ATOM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+atom_status_t atom_kv4_append(const void *k, int64_t k_token, int64_t k_head, const void *v,
+                              int64_t v_token, int64_t v_head, int64_t rows,
+                              const atom_kv4_cache_t *cache, const atom_kv4_batch_t *batch,
+                              atom_stream_t stream) {
+  return kv4_rows(true, k, k_token, k_head, v, v_token, v_head, rows, cache, batch, stream);
+}
+
+atom_status_t atom_kv4_gather(const atom_kv4_cache_t *cache, const atom_kv4_batch_t *batch,
+                              int64_t rows, void *k_out, void *v_out, atom_stream_t stream) {
+  const int64_t token = cache != nullptr ? cache->heads * 128 : 0;
+  return kv4_rows(false, k_out, token, 128, v_out, token, 128, rows, cache, batch, stream);
+}
+
+size_t atom_kv4_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads,
+                                          int64_t max_q) {
+  if (rows <= 0 || q_heads < 1 || heads < 1 || q_heads % heads != 0 || max_q < 1) return 0;
+  DeviceState *dev = nullptr;
+  if (current_device(&dev) != ATOM_OK) return 0;
+  const int nt = kv4_decode_nt(max_q < rows ? max_q : rows, q_heads / heads);
+  int ctas = 0;
+  if (kv4_decode_ctas(dev, nt, &ctas) != ATOM_OK) return 0;
+  return static_cast<size_t>(atomk::kv4_decode_cfg::ws_bytes(ctas, nt));
+}
+
+atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head, int64_t rows,
+                                 int64_t q_heads, const atom_kv4_cache_t *cache,
+                                 const atom_kv4_batch_t *batch, int32_t causal, float scale,
+                                 void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                 atom_stream_t stream) {
+  bool touched = false;
+  atom_status_t st = kv4_check_queries(rows, q_heads, scale, cache, batch, &touched);
+  if (st != ATOM_OK || !touched) return st;
+  if ((st = kv4_check_rows(q, q_token, q_head)) != ATOM_OK) return st;
+  if (!out) return ATOM_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(lse, 4)) return ATOM_ERR_ALIGN;
+  DeviceState *dev = nullptr;
+  if ((st = current_device(&dev)) != ATOM_OK) return st;
+  atomk::Kv4Attn p;
+  p.q = static_cast<const __half *>(q);
+  p.q_token = q_token;
+  p.q_head = q_head;
+  p.out = static_cast<__half *>(out);
+  p.lse = lse;
+  p.k4 = cache->k4;
+  p.v4 = cache->v4;
+  p.ks = cache->ks;
+  p.vs = cache->vs;
+  p.geom = kv4_geom(cache);
+  p.seqs = kv4_seqs(batch, cache, rows);
+  p.q_heads = static_cast<int>(q_heads);
+  p.group = static_cast<int>(q_heads / cache->heads);
+  p.scale_log2 = scale * kLog2e;
+  p.causal = causal != 0 ? 1 : 0;
+  p.max_q = static_cast<int>(batch->max_q < rows ? batch->max_q : rows);
+  using namespace atomk::kv4_decode_cfg;
+  const int nt = kv4_decode_nt(p.max_q, p.group);
+  int ctas = 0;
+  if ((st = kv4_decode_ctas(dev, nt, &ctas)) != ATOM_OK) return st;
+  p.split = workspace != nullptr && aligned(workspace, 16) &&
+            workspace_bytes >= static_cast<size_t>(ws_bytes(ctas, nt));
+  p.ws = p.split ? static_cast<float *>(workspace) : nullptr;
+  cudaError_t err = nt == 1 ? kv4_launch(atomk::kv4_decode_kernel<1>, ctas, kThreads,
+                                         smem_bytes(1), stream, p)
+                            : kv4_launch(atomk::kv4_decode_kernel<2>, ctas, kThreads,
+                                         smem_bytes(2), stream, p);
+  if (err == cudaSuccess && p.split)
+    err = nt == 1 ? kv4_launch(atomk::kv4_join_kernel<1>, ctas, atomk::kKv4JoinThreads, 0, stream, p)
+                  : kv4_launch(atomk::kv4_join_kernel<2>, ctas, atomk::kKv4JoinThreads, 0, stream, p);
+  return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
+}
+
+atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t q_head,
+                                         int64_t rows, int64_t q_heads, const float *lse,
+                                         const atom_kv4_cache_t *cache,
+                                         const atom_kv4_batch_t *batch, int32_t causal, float scale,
+                                         const float *prev, float *sums, int64_t width,
+                                         atom_stream_t stream) {
+  bool touched = false;
+  if (width < 0) return ATOM_ERR_INVALID_ARG;
+  atom_status_t st = kv4_check_queries(rows, q_heads, scale, cache, batch, &touched);
+  if (st != ATOM_OK || !touched) return st;
+  if ((st = kv4_check_rows(q, q_token, q_head)) != ATOM_OK) return st;
+  if (!lse || (!sums && width > 0)) return ATOM_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(sums, 4) || !aligned(prev, 4)) return ATOM_ERR_ALIGN;
+  DeviceState *dev = nullptr;
+  if ((st = current_device(&dev)) != ATOM_OK) return st;
+  atomk::Kv4Weights p;
+  p.q = static_cast<const __half *>(q);
+  p.q_token = q_token;
+  p.q_head = q_head;
+  p.lse = lse;
+  p.k4 = cache->k4;
+  p.ks = cache->ks;
+  p.geom = kv4_geom(cache);
+  p.seqs = kv4_seqs(batch, cache, rows);
+  if (p.seqs.capacity > width) p.seqs.capacity = static_cast<int>(width);
+  p.q_heads = static_cast<int>(q_heads);
+  p.group = static_cast<int>(q_heads / cache->heads);
+  p.scale_log2 = scale * kLog2e;
+  p.causal = causal != 0 ? 1 : 0;
+  p.prev = prev;
+  p.sums = sums;
+  p.width = width;
+  const cudaError_t err = kv4_launch(atomk::kv4_weights_kernel, 4 * dev->sm_count,
+                                     atomk::kKv4WeightThreads, 0, stream, p);
+  return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
+}
+
+atom_status_t atom_kv4_evict(const float *weights, int64_t width, const atom_kv4_cache_t *cache,
+                             const atom_kv4_batch_t *batch, int64_t budget, int64_t recent,
+                             const atom_kv4_cache_t *dst, const int32_t *to_table,
+                             int64_t to_table_stride, int64_t to_max_pages, int32_t *new_lens,
+                             int32_t *kept, float *new_weights, int64_t new_width,
+                             atom_stream_t stream) {
+  if (width < 0 || new_width < 0 || budget < 1 || recent < 0 || recent > budget)
+    return ATOM_ERR_INVALID_ARG;
+  if (!kv4_fits(budget) || (new_weights && new_width < budget)) return ATOM_ERR_SHAPE;
+  const bool touched = batch != nullptr && batch->batch > 0;
+  atom_status_t st;
+  if ((st = kv4_check_cache(cache, touched)) != ATOM_OK) return st;
+  if ((st = kv4_check_cache(dst, touched)) != ATOM_OK) return st;
+  if (cache->heads != dst->heads) return ATOM_ERR_SHAPE;
+  if ((st = kv4_check_batch(batch, false)) != ATOM_OK) return st;
+  if (!touched) return ATOM_OK;
+  if (batch->batch * cache->heads > INT32_MAX) return ATOM_ERR_SHAPE;
+  if ((st = kv4_check_table(to_table, to_table_stride, to_max_pages)) != ATOM_OK) return st;
+  if ((!weights && width > 0) || !new_lens || !kept || new_lens == batch->kv_lens)
+    return ATOM_ERR_INVALID_ARG;
+  if (new_weights == weights && new_weights != nullptr && new_width != width) return ATOM_ERR_SHAPE;
+  if (!aligned(weights, 4) || !aligned(new_lens, 4) || !aligned(kept, 4) || !aligned(new_weights, 4))
+    return ATOM_ERR_ALIGN;
+  DeviceState *dev = nullptr;
+  if ((st = current_device(&dev)) != ATOM_OK) return st;
+  atomk::Kv4Evict p;
+  p.weights = weights;
+  p.width = width;
+  p.k4 = cache->k4;
+  p.v4 = cache->v4;
+  p.ks = cache->ks;
+  p.vs = cache->vs;
+  p.geom = kv4_geom(cache);
+  p.seqs = kv4_seqs(batch, cache, 0);
+  p.to_k4 = dst->k4;
+  p.to_v4 = dst->v4;
+  p.to_ks = dst->ks;
+  p.to_vs = dst->vs;
+  p.to_geom = kv4_geom(dst);
+  p.to_table = to_table;
+  p.to_table_stride = to_table_stride;
+  p.to_capacity = kv4_capacity(to_max_pages, dst->page_size);
+  p.budget = static_cast<int>(budget);
+  p.recent = static_cast<int>(recent);
+  p.new_lens = new_lens;
+  p.kept = kept;
+  p.new_weights = new_weights;
+  p.new_width = new_width;
+  atomk::kv4_evict_kernel<<<static_cast<int>(batch->batch * cache->heads), atomk::kKv4EvictThreads,
+                            0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
+}
+
+}  // extern "C"

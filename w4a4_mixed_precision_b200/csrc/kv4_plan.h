@@ -1,0 +1,111 @@
+// kv4_plan.h -- index arithmetic of the paged INT4 KV cache: pages, sequences,
+// query rows and the division of the attention's work. Plain C++ that both the
+// kernels and a host compiler take, so that it is tested without a GPU.
+#pragma once
+
+#include <cstdint>
+
+#if defined(__CUDACC__)
+#define KV4_HD __host__ __device__ __forceinline__
+#else
+#define KV4_HD inline
+#endif
+
+namespace atomk {
+
+// Division of 0 <= n < 2^31 by a fixed 1 <= d < 2^31: with s = ceil(log2 d) and
+// m = ceil(2^(31+s) / d) < 2^32, floor(n / d) = (n * m) >> (31 + s), because
+// m * d exceeds 2^(31+s) by less than d <= 2^s and n < 2^31.
+struct Kv4Div {
+  uint32_t m, shift;
+};
+
+inline Kv4Div kv4_div_by(int64_t d) {
+  uint32_t s = 0;
+  while ((int64_t(1) << s) < d) ++s;
+  const uint64_t p = uint64_t(1) << (31 + s);
+  return Kv4Div{static_cast<uint32_t>((p + static_cast<uint64_t>(d) - 1) / static_cast<uint64_t>(d)),
+                31 + s};
+}
+
+KV4_HD int kv4_div(int n, const Kv4Div &d) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.m) >> d.shift);
+}
+
+// A cache's geometry. Vectors (one token of one head) are addressed by number:
+// vector v has its 64 bytes of codes at 64 v and its scale at v.
+struct Kv4Geom {
+  int64_t page_stride, token_stride, head_stride;   // in vectors
+  int pages, page_size, heads;
+  Kv4Div by_page;
+};
+
+// The sequences of a call. Positions are 32-bit: `capacity` is the smaller of
+// max_pages * page_size and 2^31 - 1.
+struct Kv4Seqs {
+  const int32_t *table;    // [batch][table_stride], pages of each sequence
+  int64_t table_stride;
+  const int32_t *kv_lens;  // [batch]
+  const int32_t *cu_q;     // [batch + 1]
+  int batch, rows, capacity;
+};
+
+// One sequence: rows [q0, q0 + qn) of the call are its new tokens, the last
+// qn of its `len` cached positions. `ok` is false (and qn = len = 0) where the
+// arrays on the device contradict the call's sizes; such a sequence is skipped.
+struct Kv4Seq {
+  int q0, qn, len;
+  bool ok;
+};
+
+KV4_HD Kv4Seq kv4_seq_of(int q0, int q1, int len, int rows, int capacity) {
+  Kv4Seq s{q0, q1 - q0, len, true};
+  if (q0 < 0 || q1 < q0 || q1 > rows || len < 0 || len > capacity) s = Kv4Seq{0, 0, 0, false};
+  return s;
+}
+
+// Vector number of (page, slot, head), or -1 for a page outside the cache.
+KV4_HD int64_t kv4_vector(const Kv4Geom &c, int page, int slot, int head) {
+  if (page < 0 || page >= c.pages) return -1;
+  return page * c.page_stride + slot * c.token_stride + head * c.head_stride;
+}
+
+// Cached positions a query may see: all, or (causal) those up to its own.
+KV4_HD int kv4_limit(const Kv4Seq &s, int qi, bool causal) {
+  const int64_t lim = causal ? static_cast<int64_t>(s.len) - s.qn + qi + 1 : s.len;
+  return lim < 0 ? 0 : (lim > s.len ? s.len : static_cast<int>(lim));
+}
+
+// The attention's work. The new tokens of a sequence and the `group` query
+// heads that share a KV head form qn * group query rows (row = qi * group + g),
+// cut into tiles of `tile` rows; a tile's cached positions are cut into units
+// of kKv4Unit. In the order sequence, head, tile, unit the units of a call form
+// one line, of which part i of n gets [i * total / n, (i + 1) * total / n).
+constexpr int kKv4Unit = 128;
+
+KV4_HD int kv4_tiles(const Kv4Seq &s, int group, int tile) {
+  return static_cast<int>((static_cast<int64_t>(s.qn) * group + tile - 1) / tile);
+}
+// A tile of a sequence with nothing cached still is one unit: its outputs are
+// written.
+KV4_HD int kv4_units(int len) { return len == 0 ? 1 : (len - 1) / kKv4Unit + 1; }
+
+// (= floor(i * total / parts), without the long product)
+KV4_HD int64_t kv4_part_begin(int64_t total, int parts, int i) {
+  return total / parts * i + total % parts * i / parts;
+}
+// The part that holds place `at` of the line: the largest i with
+// i * total / parts < at + 1.
+KV4_HD int kv4_part_of(int64_t total, int parts, int64_t at) {
+  return static_cast<int>(((at + 1) * parts - 1) / total);
+}
+
+// Sort key of an accumulated weight: larger weights have larger keys, the two
+// zeros the same, NaN the smallest.
+KV4_HD uint32_t kv4_weight_key(uint32_t bits) {
+  if ((bits & 0x7FFFFFFFu) > 0x7F800000u) return 0;
+  if ((bits & 0x7FFFFFFFu) == 0) bits = 0;
+  return (bits & 0x80000000u) != 0 ? ~bits : bits | 0x80000000u;
+}
+
+}  // namespace atomk
