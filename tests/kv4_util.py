@@ -85,8 +85,9 @@ def assert_within(got, want, tol, what=""):
     got = np.asarray(got, np.float64)
     same = np.isinf(want)
     assert np.array_equal(got[same], want[same]), f"{what}: infinities differ"
-    off = np.abs(got[~same] - want[~same]) - tol[~same]
-    bad = ~(off <= 0)
+    with np.errstate(invalid="ignore"):
+        off = np.abs(got[~same] - want[~same]) - tol[~same]
+    bad = ~(off <= 0) & ~(np.isinf(tol[~same]) & ~np.isnan(got[~same]))
     if bad.any():
         i = int(np.argmax(np.where(np.isnan(off), np.inf, off)))
         raise AssertionError(

@@ -113,6 +113,10 @@ def test_empty_sequences_and_rows(token_major):
     ([7, 100, 64], [7, 333, 64], 14, 2),
     ([130, 1, 257], [400, 900, 257], 4, 2),
     ([300], [300], 8, 1),
+    ([1], [1], 40, 1),
+    ([17, 0, 1, 300, 40], [17, 30, 0, 777, 20], 4, 4),
+    ([1000], [1100], 7, 1),
+    ([129, 128, 127, 33], [129, 4096, 128, 1500], 16, 8),
 ])
 def test_several_queries(new, lens, q_heads, heads, causal):
     check_attention(Call(13, new, lens, q_heads=q_heads, heads=heads, page=24, q_size=0.05),
@@ -155,11 +159,25 @@ def test_strided_queries_and_sharp_scores():
     assert_within(host(lse), want[2], want[3], "lse")
 
 
+@pytest.mark.parametrize("new", [[1, 2], [200, 60]])
 @pytest.mark.parametrize("power", [-20, 13])
-def test_values_of_any_size(power):
+def test_values_of_any_size(power, new):
     """Value scales from fp16's smallest to its largest vectors."""
-    c = Call(18, [1, 2], [400, 300], page=16, q_size=0.05)
+    c = Call(18, new, [400, 300], page=16, q_size=0.05)
     c.cache[3] = (c.cache[3] * np.float32(2.0 ** power) / np.nanmax(c.cache[3])).astype(np.float32)
+    check_attention(c)
+
+
+@pytest.mark.parametrize("new", [1, 250])
+def test_value_sizes_that_grow_and_shrink_along_the_sequence(new):
+    """Value scales that rise and fall by 2^36 over the sequence, and sharp scores: the running
+    reference has to follow what each row's own weights need."""
+    c = Call(20, [new, new], [1300, 900], q_heads=4, heads=2, page=16, q_size=0.3)
+    for b, n in enumerate(c.lens):
+        at = np.arange(n)
+        size = np.exp2(18 * np.sin(at / 150.0) - 5)[:, None].astype(np.float32)
+        place = (c.table[b, at // 16], at % 16)
+        c.cache[3][place] *= size / 8
     check_attention(c)
 
 

@@ -111,6 +111,10 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
   return cudaGetLastError() == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 
+// Largest number of query rows of a KV head that the decode kernel takes where the
+// prompt kernel runs too.
+constexpr int kKv4FewRows = 16;
+
 // Query rows a CTA of the decode kernel takes at once, 8 or 16: the smallest
 // that holds every sequence's rows of a KV head, so that the cache is read once.
 int kv4_decode_nt(int64_t max_q, int64_t group) { return max_q * group <= 8 ? 1 : 2; }
@@ -232,20 +236,37 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   p.scale_log2 = scale * kLog2e;
   p.causal = causal != 0 ? 1 : 0;
   p.max_q = static_cast<int>(batch->max_q < rows ? batch->max_q : rows);
-  using namespace atomk::kv4_decode_cfg;
-  const int nt = kv4_decode_nt(p.max_q, p.group);
-  int ctas = 0;
-  if ((st = kv4_decode_ctas(dev, nt, &ctas)) != ATOM_OK) return st;
-  p.split = workspace != nullptr && aligned(workspace, 16) &&
-            workspace_bytes >= static_cast<size_t>(ws_bytes(ctas, nt));
-  p.ws = p.split ? static_cast<float *>(workspace) : nullptr;
-  cudaError_t err = nt == 1 ? kv4_launch(atomk::kv4_decode_kernel<1>, ctas, kThreads,
-                                         smem_bytes(1), stream, p)
-                            : kv4_launch(atomk::kv4_decode_kernel<2>, ctas, kThreads,
-                                         smem_bytes(2), stream, p);
-  if (err == cudaSuccess && p.split)
-    err = nt == 1 ? kv4_launch(atomk::kv4_join_kernel<1>, ctas, atomk::kKv4JoinThreads, 0, stream, p)
-                  : kv4_launch(atomk::kv4_join_kernel<2>, ctas, atomk::kKv4JoinThreads, 0, stream, p);
+  // Sequences with up to 16 query rows a KV head go to the decode kernel, those
+  // with more to the prompt kernel; one that no sequence can need is not launched.
+  const int64_t most_rows = static_cast<int64_t>(p.max_q) * p.group;
+  const bool prompts = most_rows > kKv4FewRows, decode = !prompts || batch->batch > 1;
+  p.few_rows = !prompts ? INT32_MAX : (decode ? kKv4FewRows : 0);
+  cudaError_t err = cudaSuccess;
+  if (prompts) {
+    using namespace atomk::kv4_prompt_cfg;
+    if (!dev->kv4_prompt_attr.load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(atomk::kv4_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kSmemBytes)) != cudaSuccess)
+        return ATOM_ERR_CUDA;
+      dev->kv4_prompt_attr.store(true, std::memory_order_release);
+    }
+    err = kv4_launch(atomk::kv4_prompt_kernel, dev->sm_count, kThreads, kSmemBytes, stream, p);
+  }
+  if (err == cudaSuccess && decode) {
+    using namespace atomk::kv4_decode_cfg;
+    const int nt = kv4_decode_nt(p.max_q, p.group);
+    int ctas = 0;
+    if ((st = kv4_decode_ctas(dev, nt, &ctas)) != ATOM_OK) return st;
+    p.split = workspace != nullptr && aligned(workspace, 16) &&
+              workspace_bytes >= static_cast<size_t>(ws_bytes(ctas, nt));
+    p.ws = p.split ? static_cast<float *>(workspace) : nullptr;
+    err = nt == 1 ? kv4_launch(atomk::kv4_decode_kernel<1>, ctas, kThreads, smem_bytes(1), stream, p)
+                  : kv4_launch(atomk::kv4_decode_kernel<2>, ctas, kThreads, smem_bytes(2), stream, p);
+    if (err == cudaSuccess && p.split)
+      err = nt == 1
+                ? kv4_launch(atomk::kv4_join_kernel<1>, ctas, atomk::kKv4JoinThreads, 0, stream, p)
+                : kv4_launch(atomk::kv4_join_kernel<2>, ctas, atomk::kKv4JoinThreads, 0, stream, p);
+  }
   return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 

@@ -55,6 +55,8 @@ struct Kv4Attn {
   float scale_log2;             // scale * log2(e)
   int causal;
   int max_q;                    // largest qn of the call, as its caller says
+  int few_rows;                 // sequences of up to so many rows a KV head go to the decode
+                                // kernel, the others to the prompt kernel
   int split;                    // tiles may be shared between CTAs
   float *ws;                    // the shares (kv4_decode_cfg)
 };
@@ -190,32 +192,32 @@ __device__ __forceinline__ Kv4Seq kv4_load_seq(const Kv4Seqs &q, int b) {
                     q.capacity);
 }
 
-// This CTA's part of the line on which sequence b takes weight(b) places: where
-// it begins (sequence, places into it) and how many places it has.
-struct Kv4Part {
-  int64_t total, begin, count, rest;
-  int parts, b;
+// A place on the line on which sequence b takes weight(b) places: the line's
+// length, the sequence and the places into it (b = -1: no place was asked for).
+struct Kv4Line {
+  int64_t total, rest;
+  int b;
 };
 
-// A sum over all sequences by every CTA, each thread a run of them.
-template <int kWarps, class Weight>
-__device__ __forceinline__ Kv4Part kv4_find_part(const Kv4Seqs &seqs, const Weight &weight_of) {
+// Finds place_of(total) (negative: none). Every thread of the CTA calls it;
+// each sums a run of the sequences.
+template <int kWarps, class Weight, class Place>
+__device__ __forceinline__ Kv4Line kv4_find_place(const Kv4Seqs &seqs, const Weight &weight_of,
+                                                  const Place &place_of) {
   __shared__ int64_t warp_sums[kWarps];
-  __shared__ int64_t begin_rest;
-  __shared__ int begin_b;
+  __shared__ int64_t found_rest;
+  __shared__ int found_b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = static_cast<int>(blockIdx.x);
   const int run = (seqs.batch + 32 * kWarps - 1) / (32 * kWarps);
   const int64_t run_lo = static_cast<int64_t>(threadIdx.x) * run;
   const int b_lo = run_lo < seqs.batch ? static_cast<int>(run_lo) : seqs.batch;
   const int b_hi = seqs.batch - b_lo < run ? seqs.batch : b_lo + run;
-  auto weight = [&](int b) -> int64_t {
-    const Kv4Seq s = kv4_load_seq(seqs, b);
-    if (!s.ok && cta == 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
-    return weight_of(s);
-  };
   int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += weight(b);
+  for (int b = b_lo; b < b_hi; ++b) {
+    const Kv4Seq s = kv4_load_seq(seqs, b);
+    if (!s.ok && blockIdx.x == 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
+    mine += weight_of(s);
+  }
   int64_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -224,32 +226,52 @@ __device__ __forceinline__ Kv4Part kv4_find_part(const Kv4Seqs &seqs, const Weig
   }
   if (lane == 31) warp_sums[warp] = upto;
   __syncthreads();
-  Kv4Part part{};
+  Kv4Line line{0, 0, -1};
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) upto += warp_sums[w];
-    part.total += warp_sums[w];
+    line.total += warp_sums[w];
   }
-  const int ctas = static_cast<int>(gridDim.x);
-  part.parts = part.total < ctas ? static_cast<int>(part.total) : ctas;
-  if (cta >= part.parts) return part;   // the same for the whole CTA
-  part.begin = kv4_part_begin(part.total, part.parts, cta);
-  part.count = kv4_part_begin(part.total, part.parts, cta + 1) - part.begin;
-  if (part.begin >= upto - mine && part.begin < upto) {
-    int64_t rest = part.begin - (upto - mine);
+  const int64_t place = place_of(line.total);   // the same for the whole CTA
+  if (place < 0) return line;
+  if (place >= upto - mine && place < upto) {
+    int64_t rest = place - (upto - mine);
     for (int b = b_lo; b < b_hi; ++b) {
-      const int64_t w = weight(b);
+      const int64_t w = weight_of(kv4_load_seq(seqs, b));
       if (rest < w) {
-        begin_b = b;
-        begin_rest = rest;
+        found_b = b;
+        found_rest = rest;
         break;
       }
       rest -= w;
     }
   }
   __syncthreads();
-  part.b = begin_b;
-  part.rest = begin_rest;
+  line.b = found_b;
+  line.rest = found_rest;
+  return line;
+}
+
+// This CTA's part of the line: where it begins and how many places it has.
+struct Kv4Part {
+  int64_t total, begin, count, rest;
+  int parts, b;
+};
+
+template <int kWarps, class Weight>
+__device__ __forceinline__ Kv4Part kv4_find_part(const Kv4Seqs &seqs, const Weight &weight_of) {
+  Kv4Part part{};
+  const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+  const Kv4Line line = kv4_find_place<kWarps>(seqs, weight_of, [&](int64_t total) -> int64_t {
+    part.parts = total < ctas ? static_cast<int>(total) : ctas;
+    if (cta >= part.parts) return -1;
+    part.begin = kv4_part_begin(total, part.parts, cta);
+    part.count = kv4_part_begin(total, part.parts, cta + 1) - part.begin;
+    return part.begin;
+  });
+  part.total = line.total;
+  part.b = line.b;
+  part.rest = line.rest;
   return part;
 }
 
@@ -260,10 +282,16 @@ struct Kv4Walk {
   Kv4Seq s;
 };
 
-// Tiles per head of a sequence; none where it has more new tokens than the call
-// allows.
+// Whether a sequence has more new tokens than the call allows: it is skipped.
+__device__ __forceinline__ bool kv4_too_many(const Kv4Seq &s, const Kv4Attn &p) {
+  if (s.qn <= p.max_q) return false;
+  if (blockIdx.x == 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
+  return true;
+}
+// Tiles per head of a sequence that this kernel takes: one with few query rows.
 __device__ __forceinline__ int kv4_own_tiles(const Kv4Seq &s, const Kv4Attn &p, int tile) {
-  return s.qn > p.max_q ? 0 : kv4_tiles(s, p.group, tile);
+  if (kv4_too_many(s, p) || static_cast<int64_t>(s.qn) * p.group > p.few_rows) return 0;
+  return kv4_tiles(s, p.group, tile);
 }
 
 template <int NT>
@@ -322,7 +350,6 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
 
   // ---- this CTA's part of the line
   auto weight = [&](const Kv4Seq &q) -> int64_t {
-    if (q.qn > p.max_q && cta == 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
     return static_cast<int64_t>(kv4_own_tiles(q, p, R)) * p.geom.heads *
            (p.split ? kv4_units(q.len) : 1);
   };
