@@ -52,6 +52,7 @@ struct Kv4Attn {
   Kv4Geom geom;
   Kv4Seqs seqs;
   int q_heads, group;
+  Kv4Div by_group;
   float scale_log2;             // scale * log2(e)
   int causal;
   int max_q;                    // largest qn of the call, as its caller says

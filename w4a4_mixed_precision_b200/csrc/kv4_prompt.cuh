@@ -13,18 +13,21 @@
 // is W alone (2^-11 relative, as wide as the output's own rounding; an exact sum
 // of two halves would cost half as many matrix instructions again).
 //
-// The range of W. vs spans what the values spanned, so each KV tile's scales are
-// divided by 2^e, e the exponent of their maximum, and a row's reference R is
-// the running maximum of (row maximum of x in the tile) + e: the largest W of a
-// tile is then at most 2^15 (R lags by up to 4 before the output is rescaled,
-// W is raised by 2^11) whatever the scales are, and W keeps fp16's full
-// precision down to 2^-25 of that and an absolute error of 2^-36 of the tile's
-// largest value below. The sum of weights uses the same reference.
+// The range of W. vs spans what the values spanned, so the scales of each 32
+// tokens are divided by 2^e, e the exponent of their maximum, and a row's
+// reference R is the running maximum of (its largest x among them) + e: W is
+// then at most 2^15 (R lags by up to 8 before the output is rescaled, W is
+// raised by 2^7) whatever the scales are, and W keeps fp16's full precision
+// down to 2^-21 of R's own, and an absolute error of 2^-32 of the tokens'
+// largest value below. The sum of weights uses the same reference. (A lag of 4
+// made two warps in five rescale on every tile of the 4096-token prompt: one
+// row of 32 is enough.)
 //
-// Roles (512 threads, one CTA per SM, a persistent loop over the work):
-//   warps 0..3, 4..7   softmax of query tile 0 and 1: thread = row = TMEM lane
-//   warps 8..11        load packed tiles, expand them to fp16 operand tiles
-//   warp 12, lane 0    issues the MMAs
+// Roles (640 threads, one CTA per SM, a persistent loop over the work):
+//   warps 0..3, 4..7     softmax of query tile 0 and 1: thread = row = TMEM lane
+//   warps 8..11, 12..15  load packed keys and values, expand them to operand tiles
+//   warp 16, lane 0      issues the MMAs
+//   warps 17..19         find the work items, store their queries
 // While the tensor core multiplies for one query tile, the other tile's
 // weights are made. What bounds it: the exponentials, 16 per clock and SM (1024
 // clocks per 128x128 tile), as much as the two products (1024 clocks).
@@ -41,7 +44,13 @@
 namespace atomk {
 
 namespace kv4_prompt_cfg {
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16;
+constexpr int kQThreads = 96;        // warps 17 .. 19
+constexpr int kItems = 4;            // ring of work items
+constexpr int kItemReaders = 8 + 8 + 1 + 3;   // softmax, expanding, MMA, query warps
+// registers: 144 * 256 + 64 * 256 + 64 * 128 = 96 * 640, what the launch has
+constexpr int kSoftRegs = 144, kExpandRegs = 64, kOtherRegs = 64;
 constexpr int kRows = 256;           // query rows of a CTA's work item
 constexpr int kTok = 128;            // tokens of a KV tile
 constexpr uint32_t kTile = 128 * 256;    // an fp16 operand tile
@@ -49,14 +58,14 @@ constexpr uint32_t kHalf = kTile / 2;
 constexpr uint32_t kQOff = 1024;
 constexpr uint32_t kKOff = kQOff + 2 * kTile;
 constexpr uint32_t kVOff = kKOff + 2 * kTile;
-constexpr uint32_t kScOff = kVOff + 2 * kTile;     // 4 stages: ks, vs of 128 tokens, exponent
+constexpr uint32_t kScOff = kVOff + 2 * kTile;     // 4 stages: ks, vs of 128 tokens, 4 exponents
 constexpr uint32_t kScStage = 2 * kTok * 4 + 16;
 constexpr uint32_t kSmemBytes = kScOff + 4 * kScStage + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;       // + 128 * query tile
 constexpr uint32_t kIdescS = idesc_f16(128, 128);
 constexpr uint32_t kIdescO = idesc_f16(128, 128) | (1u << 16);   // B is MN-major
-constexpr float kRaise = 11.f, kLag = 4.f;
+constexpr float kRaise = 7.f, kLag = 8.f;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 }  // namespace kv4_prompt_cfg
 
@@ -84,7 +93,7 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                : "memory");
   asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
@@ -96,39 +105,42 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 16 bytes from shared memory, in program order with the TMEM accesses (loads
-// that the compiler moves together do not fit in the softmax's registers).
-__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+// Operand descriptors of tiles of 128-byte rows with the 128-byte swizzle, as
+// their lower words; the upper one is the same for all: 1024 bytes between
+// groups of 8 rows, descriptor version 1 (sm_100), swizzle mode 2. Kept in
+// halves, and joined where they are used, they cost the issuing thread one
+// register each. K-major: rows are MN, 64 elements of K in a row. MN-major: rows
+// are K, and blocks of 64 MN elements are `lbo` bytes apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
-// D += A * B with A (fp16) in TMEM.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+// D (+)= A * B, fp16 with an fp32 accumulator, A and B in shared memory.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
       : "memory");
 }
-
-// Descriptor of an MN-major tile stored as K rows of 128 bytes (64 elements of
-// MN) with the 128-byte swizzle: `lbo` bytes between blocks of 64 MN elements,
-// `sbo` between groups of 8 K rows.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(lbo >> 4) << 16;
-  d |= static_cast<uint64_t>(sbo >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;   // descriptor version (sm_100)
-  d |= static_cast<uint64_t>(2) << 61;   // 128-byte swizzle
-  return d;
+// The same with A (fp16 pairs, one row a lane) in TMEM.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
 }
 
 __device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
@@ -154,12 +166,14 @@ __device__ __forceinline__ uint4 codes_f16_chunk(uint32_t w) {
 }
 
 // The items of the persistent loop: query tiles of kRows rows in the order
-// sequence, tile (the last, which sees most, first), head. CTA i takes places
-// i, i + grid, ...
+// sequence, tile (the last, which sees most, first), head. Of each `grid` places
+// in turn CTA i takes the i-th, of every second turn the i-th from the end, so
+// that large and small items meet in a CTA. One thread finds them and hands them
+// on through a ring in shared memory.
 struct Kv4Item {
-  int b, head, row0, rows, kv_tiles;   // rows: query rows of the sequence and head
-  int64_t place, rest;
-  Kv4Seq s;
+  int b, head, row0, rows;   // rows: query rows of the sequence and head
+  int kv_tiles, last;        // KV tiles and cached positions that the tile's rows see
+  int q0, qn, len, more;     // more = 0: no item, the end
 };
 
 __device__ __forceinline__ int64_t kv4_prompt_weight(const Kv4Seq &s, const Kv4Attn &p) {
@@ -167,23 +181,116 @@ __device__ __forceinline__ int64_t kv4_prompt_weight(const Kv4Seq &s, const Kv4A
   return static_cast<int64_t>(kv4_tiles(s, p.group, kv4_prompt_cfg::kRows)) * p.geom.heads;
 }
 
-// The item at `rest` places into sequence it.b.
-__device__ __forceinline__ void kv4_prompt_locate(Kv4Item &it, const Kv4Attn &p) {
+// The item `rest` places into sequence b; both move on to the sequence that
+// holds it.
+__device__ __forceinline__ Kv4Item kv4_prompt_item(const Kv4Attn &p, int &b, int64_t &rest) {
   using namespace kv4_prompt_cfg;
+  Kv4Seq s;
   for (;;) {
-    it.s = kv4_load_seq(p.seqs, it.b);
-    const int64_t w = kv4_prompt_weight(it.s, p);
-    if (it.rest < w) break;
-    it.rest -= w;
-    ++it.b;
+    s = kv4_load_seq(p.seqs, b);
+    const int64_t w = kv4_prompt_weight(s, p);
+    if (rest < w) break;
+    rest -= w;
+    ++b;
   }
-  it.rows = it.s.qn * p.group;
-  const int tiles = kv4_tiles(it.s, p.group, kRows);
-  const int at = static_cast<int>(it.rest / p.geom.heads);
-  it.head = static_cast<int>(it.rest - static_cast<int64_t>(at) * p.geom.heads);
+  Kv4Item it;
+  it.b = b;
+  it.rows = s.qn * p.group;
+  const int tiles = kv4_tiles(s, p.group, kRows);
+  const int at = static_cast<int>(rest / p.geom.heads);
+  it.head = static_cast<int>(rest - static_cast<int64_t>(at) * p.geom.heads);
   it.row0 = (tiles - 1 - at) * kRows;
-  const int last = (it.row0 + kRows < it.rows ? it.row0 + kRows : it.rows) - 1;
-  it.kv_tiles = (kv4_limit(it.s, last / p.group, p.causal != 0) + kTok - 1) / kTok;
+  const int last_row = (it.rows - it.row0 > kRows ? it.row0 + kRows : it.rows) - 1;
+  it.last = kv4_limit(s, last_row / p.group, p.causal != 0);
+  it.kv_tiles = (it.last + kTok - 1) / kTok;
+  it.q0 = s.q0;
+  it.qn = s.qn;
+  it.len = s.len;
+  it.more = 1;
+  return it;
+}
+
+// The two passes over a row's 128 scores. Both are short loops: unrolled, the
+// roles' code together does not stay in the instruction caches (half of the
+// softmax's time went into waiting for instructions). `sc`, in shared memory:
+// ks, vs (scaled by 2^-e) and the four e's, one per 32 tokens.
+
+// Largest score of a row, each plus its e: what the reference follows.
+template <bool kMask>
+__device__ __forceinline__ float kv4_row_max(uint32_t s_addr, const float4 *sc, int seen) {
+  using namespace kv4_prompt_cfg;
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t raw[32];
+    tmem_ld_x32(s_addr + 32 * c, raw);
+    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    const float e = reinterpret_cast<const float *>(sc + 2 * kTok / 4)[c];
+    tmem_ld_wait(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 k = sc[8 * c + i];
+      float2 x = f2_mul(make_float2(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1])),
+                        make_float2(k.x, k.y));
+      float2 y = f2_mul(make_float2(__uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3])),
+                        make_float2(k.z, k.w));
+      if (kMask) {
+        const int left = seen - 32 * c - 4 * i;
+        if (left <= 0) x.x = -INFINITY;
+        if (left <= 1) x.y = -INFINITY;
+        if (left <= 2) y.x = -INFINITY;
+        if (left <= 3) y.y = -INFINITY;
+      }
+      m4[2 * (i & 1)] = fmaxf(m4[2 * (i & 1)], fmaxf(x.x, x.y));
+      m4[2 * (i & 1) + 1] = fmaxf(m4[2 * (i & 1) + 1], fmaxf(y.x, y.y));
+    }
+    mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) + e);
+  }
+  return mx;
+}
+
+// Weights in the reference `top`, times the value scales, as fp16 pairs over the
+// scores (columns 16c .. of W are columns 32c .. of S, which have been read by
+// then). Returns the sum of the weights.
+template <bool kMask>
+__device__ __forceinline__ float kv4_row_weights(uint32_t s_addr, const float4 *sc, float top,
+                                                 int seen) {
+  using namespace kv4_prompt_cfg;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t raw[32], packed[16];
+    tmem_ld_x32(s_addr + 32 * c, raw);
+    const float e = reinterpret_cast<const float *>(sc + 2 * kTok / 4)[c];
+    const float add = e + kRaise - top, back = exp2_approx(-e - kRaise);
+    const float2 add2 = make_float2(add, add);
+    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    tmem_ld_wait(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 k = sc[8 * c + i], v = sc[kTok / 4 + 8 * c + i];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t *r = &raw[4 * i + 2 * h];
+        float2 y = f2_fma(make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])),
+                          h == 0 ? make_float2(k.x, k.y) : make_float2(k.z, k.w), add2);
+        y.x = exp2_approx(y.x);
+        y.y = exp2_approx(y.y);
+        if (kMask) {
+          const int left = seen - 32 * c - 4 * i - 2 * h;
+          if (left <= 0) y.x = 0.f;
+          if (left <= 1) y.y = 0.f;
+        }
+        part[h] = f2_add(part[h], y);
+        y = f2_mul(y, h == 0 ? make_float2(v.x, v.y) : make_float2(v.z, v.w));
+        packed[2 * i + h] = pack_half2_rn(y.x, y.y);
+      }
+    }
+    tmem_st_x16(s_addr + 16 * c, packed);
+    const float2 both = f2_add(part[0], part[1]);
+    sum = fmaf(both.x + both.y, back, sum);
+  }
+  return sum;
 }
 
 __global__ void __launch_bounds__(kv4_prompt_cfg::kThreads, 1)
@@ -192,22 +299,26 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem);   // [2] query tile stored
-  uint64_t *s_full = q_full + 2;    // [2] S of the query tile complete
+  uint64_t *q_empty = q_full + 2;   // [2] its last product complete
+  uint64_t *s_full = q_empty + 2;   // [2] S of the query tile complete
   uint64_t *p_full = s_full + 2;    // [2] W stored over S (and O rescaled)
   uint64_t *o_full = p_full + 2;    // [2] W V complete
   uint64_t *k_full = o_full + 2;    // [2] key tile expanded
   uint64_t *k_empty = k_full + 2;   // [2] both products with it complete
   uint64_t *v_full = k_empty + 2;
   uint64_t *v_empty = v_full + 2;
-  uint64_t *done = v_empty + 2;
+  uint64_t *item_full = v_empty + 2;         // [kItems]
+  uint64_t *item_empty = item_full + kItems; // [kItems] read by every role
+  uint64_t *done = item_empty + kItems;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  uint32_t *tile_max = tmem_slot + 4;   // [2][4] largest value scale of each expanding warp
+  Kv4Item *ring = reinterpret_cast<Kv4Item *>(tmem_slot + 2);   // [kItems]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 128);
+      mbar_init(&q_full[i], kQThreads);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
@@ -216,18 +327,24 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
       mbar_init(&v_full[i], 128);
       mbar_init(&v_empty[i], 1);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kItemReaders);
+    }
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
   grid_dependency_wait();
   const Kv4Line line = kv4_find_place<kThreads / 32>(
       p.seqs, [&](const Kv4Seq &s) { return kv4_prompt_weight(s, p); },
-      [](int64_t total) -> int64_t { return blockIdx.x < total ? static_cast<int64_t>(blockIdx.x) : -1; });
+      [](int64_t total) -> int64_t {
+        return blockIdx.x < total ? static_cast<int64_t>(blockIdx.x) : -1;
+      });
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -236,17 +353,23 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     report_status(6 /* ATOM_ERR_TIMEOUT */);
     *abort_flag = 1;
   };
-  Kv4Item it;
-  it.place = blockIdx.x;
-  it.b = line.b;
-  it.rest = line.rest;
-  auto next_item = [&]() {
-    it.place += gridDim.x;
-    it.rest += gridDim.x;
+  // The next item for a warp (or a lone thread), in turn; false: a wait gave up.
+  uint32_t item_no = 0;
+  auto take_item = [&](Kv4Item &it, bool whole_warp) -> bool {
+    const int slot = item_no % kItems;
+    bool ok = mbar_wait_inline(&item_full[slot], (item_no / kItems) & 1, abort_flag);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    it = ring[slot];
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(&item_empty[slot]);
+    ++item_no;
+    return true;
   };
 
   if (warp < 8) {
     // ================================================================ softmax
+    regs_increase<kSoftRegs>();
     const int w = warp >> 2;                     // query tile
     const int tid = threadIdx.x & 127;           // row of it, TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -254,77 +377,38 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     const uint32_t o_addr = tbase + lane_base + kTmemO + 128 * w;
     uint32_t tiles = 0;                          // KV tiles so far, over all items
     bool ok = true;
-    for (; ok && it.place < line.total; next_item()) {
-      kv4_prompt_locate(it, p);
+    for (;;) {
+      Kv4Item it;
+      if (!(ok = take_item(it, true)) || !it.more) break;
       const int r = it.row0 + 128 * w + tid;
       const bool valid = r < it.rows;
-      const int qi = valid ? r / p.group : 0;
+      const int qi = valid ? kv4_div(r, p.by_group) : 0;
       const int hq = it.head * p.group + (valid ? r - qi * p.group : 0);
-      const int limit = valid ? kv4_limit(it.s, qi, p.causal != 0) : 0;
+      // (a row past the last computes on zeros and is not written)
+      const int limit =
+          valid ? kv4_limit(Kv4Seq{it.q0, it.qn, it.len, true}, qi, p.causal != 0) : INT32_MAX;
       const int n = it.kv_tiles;
       float top = kKv4NoMax, sum = 0.f;
-      if (n > 0) {
-        // ---- this row of Q, in the codes' order
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (it.s.q0 + qi) * p.q_token +
-                                                           hq * p.q_head);
-        uint8_t *dst = smem + kQOff + w * kTile + tid * 128;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-          st_shared_v4(dst + (c >> 3) * kHalf + (((c & 7) ^ (tid & 7)) << 4),
-                       __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[w]);
-      }
       for (int j = 0; j < n; ++j, ++tiles) {
-        if (!__all_sync(0xffffffffu, mbar_wait_inline(&s_full[w], tiles & 1, abort_flag))) {
-          ok = false;
-          break;
-        }
+        ok = mbar_wait_inline(&v_full[tiles & 1], (tiles >> 1) & 1, abort_flag) &&
+             mbar_wait_inline(&s_full[w], tiles & 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
-        const uint8_t *sc = smem + kScOff + (tiles & 3) * kScStage;
-        const uint32_t ks = smem_addr(sc), vs = ks + kTok * 4;
-        const float e = *reinterpret_cast<const float *>(sc + 2 * kTok * 4);
-        float4 kq;
+        const float4 *sc = reinterpret_cast<const float4 *>(smem + kScOff + (tiles & 3) * kScStage);
         const int seen = limit - j * kTok;   // columns of this tile that the row sees
         const bool mask = __any_sync(0xffffffffu, seen < kTok);
-        // ---- first pass over S: the maximum. (S is read again below: 128
-        // scores a thread do not fit beside the rest of its registers.)
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t raw[32];
-          tmem_ld_x32(s_addr + 32 * c, raw);
-          tmem_ld_wait(raw);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 k;
-            if ((i & 1) == 0) kq = ld_shared_v4(ks + 16 * (8 * c + i / 2));
-            k = (i & 1) == 0 ? make_float2(kq.x, kq.y) : make_float2(kq.z, kq.w);
-            float2 x = f2_mul(
-                make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1])), k);
-            if (mask) {
-              if (32 * c + 2 * i >= seen) x.x = -INFINITY;
-              if (32 * c + 2 * i + 1 >= seen) x.y = -INFINITY;
-            }
-            m4[i & 3] = fmaxf(m4[i & 3], fmaxf(x.x, x.y));
-          }
-        }
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        if (__any_sync(0xffffffffu, mx + e > top + kLag)) {
-          const float up = fmaxf(top, mx + e);
+        const float mx = mask ? kv4_row_max<true>(s_addr, sc, seen)
+                              : kv4_row_max<false>(s_addr, sc, seen);
+        if (__any_sync(0xffffffffu, mx > top + kLag)) {
+          const float up = fmaxf(top, mx);
           const float f = exp2_approx(top - up);
           top = up;
           sum *= f;
           if (j > 0) {   // the output so far, in the new reference
-            if (!__all_sync(0xffffffffu, mbar_wait_inline(&o_full[w], (tiles - 1) & 1, abort_flag))) {
-              ok = false;
-              break;
-            }
+            ok = mbar_wait_inline(&o_full[w], (tiles - 1) & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               uint32_t o[16];
               tmem_ld_x16(o_addr + 16 * c, o);
@@ -335,57 +419,22 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
             }
           }
         }
-        const float add = e + kRaise - top;
-        const float2 add2 = make_float2(add, add);
-        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // ---- second pass: weights, their sum, and W over S (columns 16c .. of W
-        // are columns 32c .. of S, which has been read by then)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t raw[32], packed[16];
-          tmem_ld_x32(s_addr + 32 * c, raw);
-          tmem_ld_wait(raw);
-          float4 v;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const bool even = (i & 1) == 0;
-            if (even) {
-              kq = ld_shared_v4(ks + 16 * (8 * c + i / 2));
-              v = ld_shared_v4(vs + 16 * (8 * c + i / 2));
-            }
-            float2 y = f2_fma(
-                make_float2(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1])),
-                even ? make_float2(kq.x, kq.y) : make_float2(kq.z, kq.w), add2);
-            y.x = exp2_approx(y.x);
-            y.y = exp2_approx(y.y);
-            if (mask) {
-              if (32 * c + 2 * i >= seen) y.x = 0.f;
-              if (32 * c + 2 * i + 1 >= seen) y.y = 0.f;
-            }
-            part[i & 1] = f2_add(part[i & 1], y);
-            y = f2_mul(y, even ? make_float2(v.x, v.y) : make_float2(v.z, v.w));
-            packed[i] = pack_half2_rn(y.x, y.y);
-          }
-          tmem_st_x16(s_addr + 16 * c, packed);
-        }
-        const float2 both = f2_add(part[0], part[1]);
-        sum += (both.x + both.y) * exp2_approx(-e - kRaise);
+        sum += mask ? kv4_row_weights<true>(s_addr, sc, top, seen)
+                    : kv4_row_weights<false>(s_addr, sc, top, seen);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(&p_full[w]);
       }
       if (!ok) break;
       // ---- the rows' outputs
-      const int64_t row = static_cast<int64_t>(it.s.q0 + qi) * p.q_heads + hq;
+      const int64_t row = static_cast<int64_t>(it.q0 + qi) * p.q_heads + hq;
       const float inv = sum > 0.f ? __fdiv_rn(exp2_approx(-kRaise), sum) : 0.f;
       if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait_inline(&o_full[w], (tiles - 1) & 1, abort_flag))) {
-          ok = false;
-          break;
-        }
+        ok = mbar_wait_inline(&o_full[w], (tiles - 1) & 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
       }
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         if (n > 0) {
@@ -410,160 +459,216 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
       tc_fence_before_sync();
     }
     if (!ok && lane == 0) fail();
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ================================================================ expand
-    const int ew = warp - 8, g = lane >> 2, t = lane & 3;
+    regs_decrease<kExpandRegs>();
+    const bool value = warp >= 12;   // warps 8..11 keys, 12..15 values
+    const int ew = warp & 3, g = lane >> 2, t = lane & 3;
+    const uint8_t *codes = value ? p.v4 : p.k4;
+    const float *scales = value ? p.vs : p.ks;
+    uint64_t *full = value ? v_full : k_full, *empty = value ? v_empty : k_empty;
+    uint8_t *tile0 = smem + (value ? kVOff : kKOff);
     uint32_t tiles = 0;
     bool ok = true;
-    uint4 kq[4], vq[4];
-    float ks = 0.f, vs = 0.f;
-    int64_t last = 0;   // cached positions that the item's rows see
-    auto load = [&](int j) {
-      const int pos = j * kTok + 32 * ew + lane;
-      int64_t vec = -1;
-      ks = vs = 0.f;
-      if (pos < last) {
-        const int page_no = kv4_div(pos, p.geom.by_page);
-        const int page = __ldg(p.seqs.table + it.b * p.seqs.table_stride + page_no);
-        vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, it.head);
-        if (vec < 0) {
-          report_status(1 /* ATOM_ERR_INVALID_ARG */);
-        } else {
-          ks = __ldg(p.ks + vec) * p.scale_log2;
-          vs = __ldg(p.vs + vec);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {   // chunk t of token 8i + g
-        const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
-        kq[i] = vq[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (v >= 0) {
-          kq[i] = __ldg(reinterpret_cast<const uint4 *>(p.k4 + v * 64 + t * 16));
-          vq[i] = __ldg(reinterpret_cast<const uint4 *>(p.v4 + v * 64 + t * 16));
-        }
-      }
-    };
-    auto expand = [&](const uint4 (&q)[4], uint8_t *tile) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 32 * ew + 8 * i + g;
-        uint8_t *dst = tile + (t >> 1) * kHalf + row * 128;
-        const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 c = codes_f16_chunk(words[k]);
-          st_shared_v4(dst + (((4 * (t & 1) + k) ^ (row & 7)) << 4), c.x, c.y, c.z, c.w);
-        }
-      }
-      fence_proxy_async_smem();
-    };
-    for (; ok && it.place < line.total; next_item()) {
-      kv4_prompt_locate(it, p);
+    for (;;) {
+      Kv4Item it;
+      if (!(ok = take_item(it, true)) || !it.more) break;
       const int n = it.kv_tiles;
-      const int last_row = (it.row0 + kRows < it.rows ? it.row0 + kRows : it.rows) - 1;
-      last = kv4_limit(it.s, last_row / p.group, p.causal != 0);
-      if (n > 0) load(0);
+      const int32_t *table = p.seqs.table + it.b * p.seqs.table_stride;
+      int page_no = 0, page = -1;      // of the token whose address is made next
+      auto fetch_page = [&](int j) {
+        const int pos = j * kTok + 32 * ew + lane;
+        page_no = kv4_div(pos, p.geom.by_page);
+        page = pos < it.last ? __ldg(table + page_no) : -1;
+      };
+      uint4 q[4];
+      float scale = 0.f;
+      auto load = [&](int j) {
+        const int pos = j * kTok + 32 * ew + lane;
+        int64_t vec = -1;
+        scale = 0.f;
+        if (pos < it.last) {
+          vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, it.head);
+          if (vec < 0)
+            report_status(1 /* ATOM_ERR_INVALID_ARG */);
+          else
+            scale = __ldg(scales + vec);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // chunk t of token 8i + g
+          const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
+          q[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (v >= 0) q[i] = __ldg(reinterpret_cast<const uint4 *>(codes + v * 64 + t * 16));
+        }
+      };
+      if (n > 0) {
+        fetch_page(0);
+        load(0);
+        if (n > 1) fetch_page(1);
+      }
       for (int j = 0; j < n; ++j, ++tiles) {
         const int st = tiles & 1;
-        const uint32_t ph = (tiles >> 1) & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[st], ph ^ 1u, abort_flag))) {
-          ok = false;
-          break;
+        ok = mbar_wait_inline(&empty[st], ((tiles >> 1) & 1) ^ 1u, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        // scales of this warp's 32 tokens, those of the values divided by 2^e
+        // (the stage of scales was last read four tiles ago)
+        float *sc = reinterpret_cast<float *>(smem + kScOff + (tiles & 3) * kScStage);
+        if (value) {
+          const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(scale));
+          int e = static_cast<int>(largest >> 23) - 126;   // every scale < 2^e
+          e = e < -60 ? -60 : (e > 100 ? 100 : e);
+          sc[kTok + 32 * ew + lane] = scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          if (lane == 0) sc[2 * kTok + ew] = static_cast<float>(e);
+        } else {
+          sc[32 * ew + lane] = scale * p.scale_log2;
         }
-        // the stage's scales were last read four tiles ago
-        uint8_t *sc = smem + kScOff + (tiles & 3) * kScStage;
-        const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
-        if (lane == 0) tile_max[4 * st + ew] = largest;
-        expand(kq, smem + kKOff + st * kTile);
-        named_bar_sync(1, 128);
-        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = tile_max[4 * st + i] > m ? tile_max[4 * st + i] : m;
-        int e = static_cast<int>(m >> 23) - 126;   // m < 2^e
-        e = e < -60 ? -60 : (e > 100 ? 100 : e);
-        reinterpret_cast<float *>(sc)[32 * ew + lane] = ks;
-        reinterpret_cast<float *>(sc)[kTok + 32 * ew + lane] =
-            vs * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        if (threadIdx.x == 8 * 32)
-          *reinterpret_cast<float *>(sc + 2 * kTok * 4) = static_cast<float>(e);
-        mbar_arrive(&k_full[st]);
-        if (!__all_sync(0xffffffffu, mbar_wait(&v_empty[st], ph ^ 1u, abort_flag))) {
-          ok = false;
-          break;
+        for (int i = 0; i < 4; ++i) {
+          const int row = 32 * ew + 8 * i + g;
+          uint8_t *dst = tile0 + st * kTile + (t >> 1) * kHalf + row * 128;
+          const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 c = codes_f16_chunk(words[k]);
+            st_shared_v4(dst + (((4 * (t & 1) + k) ^ (row & 7)) << 4), c.x, c.y, c.z, c.w);
+          }
         }
-        expand(vq, smem + kVOff + st * kTile);
-        mbar_arrive(&v_full[st]);
-        if (j + 1 < n) load(j + 1);
+        fence_proxy_async_smem();
+        mbar_arrive(&full[st]);
+        if (j + 1 < n) {
+          load(j + 1);
+          if (j + 2 < n) fetch_page(j + 2);
+        }
       }
+      if (!ok) break;
     }
     if (!ok && lane == 0) fail();
   } else {
-    // ================================================================ MMA issuer
-    if (warp == 12 && lane == 0) {
+    regs_decrease<kOtherRegs>();
+    if (warp > kMmaWarp) {
+      // ============================================================== queries
+      // Finds the items (first warp, one thread) and stores their query rows in
+      // the order of the codes, as soon as the tile's last product with the
+      // previous ones is complete.
+      int b = line.b, turn = 0;
+      int64_t place = blockIdx.x, rest = line.rest;
+      uint32_t loads = 0, made = 0;
+      auto make_item = [&]() -> bool {   // one thread
+        const int slot = made % kItems;
+        if (!mbar_wait_inline(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag)) return false;
+        Kv4Item it{};
+        if (place < line.total) {
+          it = kv4_prompt_item(p, b, rest);
+          const int grid = static_cast<int>(gridDim.x), i = static_cast<int>(blockIdx.x);
+          const int step = ++turn & 1 ? 2 * (grid - 1 - i) + 1 : 2 * i + 1;
+          place += step;
+          rest += step;
+        }
+        ring[slot] = it;
+        mbar_arrive(&item_full[slot]);
+        ++made;
+        return true;
+      };
+      bool ok = true;
+      const int qt = threadIdx.x - 32 * (kMmaWarp + 1);   // 0 .. kQThreads - 1
+      if (qt == 0) ok = make_item();
+      for (;;) {
+        // one item ahead, so that no role waits for the search
+        if (qt == 0 && ok && ring[(made - 1) % kItems].more) ok = make_item();
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        Kv4Item it;
+        if (!(ok = take_item(it, true)) || !it.more) break;
+        if (it.kv_tiles == 0) continue;
+        for (int w = 0; w < 2; ++w) {
+          ok = mbar_wait_inline(&q_empty[w], (loads & 1) ^ 1u, abort_flag);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          // 16 lanes a row, a 16-byte chunk each
+          for (int i0 = qt; i0 < 128 * 16; i0 += 8 * kQThreads) {
+            uint4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int i = i0 + u * kQThreads, r = it.row0 + 128 * w + (i >> 4);
+              x[u] = make_uint4(0u, 0u, 0u, 0u);
+              if (i < 128 * 16 && r < it.rows) {
+                const int qi = kv4_div(r, p.by_group), hq = it.head * p.group + r - qi * p.group;
+                x[u] = __ldg(reinterpret_cast<const uint4 *>(p.q + (it.q0 + qi) * p.q_token +
+                                                             hq * p.q_head) + (i & 15));
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int i = i0 + u * kQThreads, row = i >> 4, c = i & 15;
+              if (i < 128 * 16)
+                st_shared_v4(smem + kQOff + w * kTile + (c >> 3) * kHalf + row * 128 +
+                                 (((c & 7) ^ (row & 7)) << 4),
+                             __byte_perm(x[u].x, x[u].z, 0x5410), __byte_perm(x[u].x, x[u].z, 0x7632),
+                             __byte_perm(x[u].y, x[u].w, 0x5410), __byte_perm(x[u].y, x[u].w, 0x7632));
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&q_full[w]);
+        }
+        if (!ok) break;
+        ++loads;
+      }
+      if (!ok && lane == 0) fail();
+    } else if (lane == 0) {
+      // ============================================================== MMA issuer
       uint32_t tiles = 0, items = 0;
       bool ok = true;
-      const uint32_t q_addr = smem_addr(smem + kQOff), k_addr = smem_addr(smem + kKOff);
-      const uint32_t v_addr = smem_addr(smem + kVOff);
-      auto scores = [&](int w, int st) {
+      const uint32_t q_lo = desc_lo_k(smem_addr(smem + kQOff));
+      const uint32_t k_lo = desc_lo_k(smem_addr(smem + kKOff));
+      const uint32_t v_lo = desc_lo_mn(smem_addr(smem + kVOff), kHalf);
+      auto scores = [&](int w, int st, bool last) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-          mma_f16(tbase + kTmemS + 128 * w, smem_desc_k_sw128(q_addr + w * kTile + off),
-                  smem_desc_k_sw128(k_addr + st * kTile + off), kIdescS, k > 0 ? 1u : 0u);
+          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+          mma_f16_ss(tbase + kTmemS + 128 * w, q_lo + w * (kTile >> 4) + off,
+                     k_lo + st * (kTile >> 4) + off, kIdescS, k > 0 ? 1u : 0u);
         }
         tc_commit(&s_full[w]);
+        if (last) tc_commit(&q_empty[w]);
+        if (w == 1) tc_commit(&k_empty[st]);
       };
       auto outputs = [&](int w, int st, bool first) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           mma_f16_ts(tbase + kTmemO + 128 * w, tbase + kTmemS + 128 * w + 8 * k,
-                     smem_desc_mn_sw128(v_addr + st * kTile + k * 2048, kHalf, 1024), kIdescO,
+                     v_lo + st * (kTile >> 4) + k * (2048 >> 4), kIdescO,
                      !first || k > 0 ? 1u : 0u);
         tc_commit(&o_full[w]);
+        if (w == 1) tc_commit(&v_empty[st]);
       };
-      for (; ok && it.place < line.total; next_item()) {
-        kv4_prompt_locate(it, p);
+      for (;;) {
+        Kv4Item it;
+        if (!(ok = take_item(it, false)) || !it.more) break;
         const int n = it.kv_tiles;
         if (n == 0) continue;
-        if (!mbar_wait(&k_full[tiles & 1], (tiles >> 1) & 1, abort_flag) ||
-            !mbar_wait(&q_full[0], items & 1, abort_flag) ||
-            !mbar_wait(&q_full[1], items & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        scores(0, tiles & 1);
-        scores(1, tiles & 1);
-        tc_commit(&k_empty[tiles & 1]);
-        for (int j = 0; j < n; ++j, ++tiles) {
-          const int st = tiles & 1, nst = (tiles + 1) & 1;
-          if (!mbar_wait(&v_full[st], (tiles >> 1) & 1, abort_flag) ||
-              !mbar_wait(&p_full[0], tiles & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          outputs(0, st, j == 0);
-          if (j + 1 < n) {
-            if (!mbar_wait(&k_full[nst], ((tiles + 1) >> 1) & 1, abort_flag)) {
-              ok = false;
-              break;
+        // step j: W V of tile j - 1, then Q K^T of tile j, for one query tile
+        // and then the other
+        for (int j = 0; ok && j <= n; ++j) {
+          const int st = tiles & 1, pst = (tiles - 1) & 1;
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            if (j > 0) {
+              ok = (w != 0 || mbar_wait(&v_full[pst], ((tiles - 1) >> 1) & 1, abort_flag)) &&
+                   mbar_wait(&p_full[w], (tiles - 1) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after_sync();
+              outputs(w, pst, j == 1);
+            } else {
+              ok = mbar_wait(&q_full[w], items & 1, abort_flag);
+              if (!ok) break;
             }
-            tc_fence_after_sync();
-            scores(0, nst);
+            if (j < n) {
+              if (w == 0 && !(ok = mbar_wait(&k_full[st], (tiles >> 1) & 1, abort_flag))) break;
+              tc_fence_after_sync();
+              scores(w, st, j + 1 == n);
+            }
           }
-          if (!mbar_wait(&p_full[1], tiles & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          outputs(1, st, j == 0);
-          tc_commit(&v_empty[st]);
-          if (j + 1 < n) {
-            scores(1, nst);
-            tc_commit(&k_empty[nst]);
-          }
+          if (j < n) ++tiles;
         }
+        if (!ok) break;
         ++items;
       }
       if (!ok) fail();
@@ -575,7 +680,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tbase, kTmemCols);
   }
