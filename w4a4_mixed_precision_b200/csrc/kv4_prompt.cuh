@@ -3,11 +3,14 @@
 // formulas are kv4_attn.cuh's.
 //
 // A CTA takes 256 query rows of a (sequence, KV head) as two tiles of 128, and
-// the cached tokens that they see in tiles of 128. Per KV tile and query tile:
-//   S = Q K^T     128x128x128, fp16 codes of K from shared memory, fp32 S in TMEM
+// the cached tokens that they see in tiles of 64. Per KV tile and query tile:
+//   S = Q K^T     128x64x128, fp16 codes of K from shared memory, fp32 S in TMEM
 //   W = 2^(x - R) * vs, x = S * ks * scale * log2(e)   (one thread a row; fp16, into TMEM
 //                                                       over S)
-//   O += W V      128x128x128, W from TMEM, codes of V from shared memory
+//   O += W V      128x128x64, W from TMEM, codes of V from shared memory
+// S has two buffers a query tile, so that the scores of the next KV tile are
+// there when a row's weights are done (with tiles of 128 tokens TMEM, 512
+// columns, has room for one, and the softmax waited for the tensor core).
 // The codes are exact in fp16 and every scale belongs to a token, that is to a
 // column of S and W, so it multiplies there, in fp32. What is rounded to 16 bits
 // is W alone (2^-11 relative, as wide as the output's own rounding; an exact sum
@@ -26,17 +29,17 @@
 // Roles (640 threads, one CTA per SM, a persistent loop over the work):
 //   warps 0..3, 4..7     softmax of query tile 0 and 1: thread = row = TMEM lane
 //   warps 8..11, 12..15  load packed keys and values, expand them to operand tiles
-//   warp 16, lane 0      issues the MMAs
-//   warps 17..19         find the work items, store their queries
+//   warps 16, 17         issue the MMAs of query tile 0 and 1
+//   warps 18, 19         find the work items, copy their queries
 // While the tensor core multiplies for one query tile, the other tile's
 // weights are made. What bounds it: the exponentials, 16 per clock and SM (1024
 // clocks per 128x128 tile), as much as the two products (1024 clocks).
 //
 // Operand layouts. K and V tiles are 128 rows (tokens) of 256 bytes as two
 // halves of 128-byte rows with the 128-byte swizzle: for S they are a K-major B
-// operand, for O an MN-major one. A word of 8 codes becomes one 16-byte chunk
-// in the order 0 4 1 5 2 6 3 7 that masking gives; Q's chunks are stored in the
-// same order, and the epilogue undoes it for the output's columns.
+// operand, for O an MN-major one. A word of 8 codes becomes one 16-byte chunk:
+// of keys in its own order, as the queries are copied; of values in the order
+// 0 4 1 5 2 6 3 7 that masking gives, which the epilogue undoes.
 #pragma once
 
 #include "kv4_attn.cuh"
@@ -45,25 +48,29 @@ namespace atomk {
 
 namespace kv4_prompt_cfg {
 constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16;
-constexpr int kQThreads = 96;        // warps 17 .. 19
+constexpr int kMmaWarp = 16;         // and 17: one for each query tile
+constexpr int kQWarp = 18;           // and 19
+constexpr int kQThreads = 64;
 constexpr int kItems = 4;            // ring of work items
-constexpr int kItemReaders = 8 + 8 + 1 + 3;   // softmax, expanding, MMA, query warps
+constexpr int kItemReaders = 8 + 8 + 2 + 2;   // softmax, expanding, MMA, query warps
 // registers: 144 * 256 + 64 * 256 + 64 * 128 = 96 * 640, what the launch has
 constexpr int kSoftRegs = 144, kExpandRegs = 64, kOtherRegs = 64;
 constexpr int kRows = 256;           // query rows of a CTA's work item
-constexpr int kTok = 128;            // tokens of a KV tile
-constexpr uint32_t kTile = 128 * 256;    // an fp16 operand tile
-constexpr uint32_t kHalf = kTile / 2;
+constexpr int kTok = 64;             // tokens of a KV tile
+constexpr int kStages = 4;           // of key and of value tiles
+constexpr int kScStages = 8;         // of their scales
+constexpr uint32_t kQTile = 128 * 256, kQHalf = kQTile / 2;   // fp16 operand tiles
+constexpr uint32_t kTile = kTok * 256, kHalf = kTile / 2;
 constexpr uint32_t kQOff = 1024;
-constexpr uint32_t kKOff = kQOff + 2 * kTile;
-constexpr uint32_t kVOff = kKOff + 2 * kTile;
-constexpr uint32_t kScOff = kVOff + 2 * kTile;     // 4 stages: ks, vs of 128 tokens, 4 exponents
+constexpr uint32_t kKOff = kQOff + 2 * kQTile;
+constexpr uint32_t kVOff = kKOff + kStages * kTile;
+constexpr uint32_t kScOff = kVOff + kStages * kTile;   // ks, vs of a tile's tokens, 2 exponents
 constexpr uint32_t kScStage = 2 * kTok * 4 + 16;
-constexpr uint32_t kSmemBytes = kScOff + 4 * kScStage + 1024;   // + alignment slack
+constexpr uint32_t kOutOff = kScOff + kScStages * kScStage;      // 2 KB for each softmax warp
+constexpr uint32_t kSmemBytes = kOutOff + 8 * 2048 + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 0, kTmemO = 256;       // + 128 * query tile
-constexpr uint32_t kIdescS = idesc_f16(128, 128);
+constexpr uint32_t kTmemS = 0, kTmemO = 256;       // + 128 * query tile; S + 64 * (tile & 1)
+constexpr uint32_t kIdescS = idesc_f16(128, kTok);
 constexpr uint32_t kIdescO = idesc_f16(128, 128) | (1u << 16);   // B is MN-major
 constexpr float kRaise = 7.f, kLag = 8.f;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -119,6 +126,17 @@ __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t lbo) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // D (+)= A * B, fp16 with an fp32 accumulator, A and B in shared memory.
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                            uint32_t idesc, uint32_t accumulate) {
@@ -158,11 +176,14 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
   return d;
 }
 
-// A word of codes as a 16-byte chunk, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ uint4 codes_f16_chunk(uint32_t w) {
+// A word of codes as a 16-byte chunk: in the order 0 4 1 5 2 6 3 7 that masking
+// gives, or in its own.
+__device__ __forceinline__ uint4 codes_f16_chunk(uint32_t w, bool in_order) {
   uint32_t o[4];
   codes_f16_word(w, o);
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  if (!in_order) return make_uint4(o[0], o[1], o[2], o[3]);
+  return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                    __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
 }
 
 // The items of the persistent loop: query tiles of kRows rows in the order
@@ -210,77 +231,69 @@ __device__ __forceinline__ Kv4Item kv4_prompt_item(const Kv4Attn &p, int &b, int
   return it;
 }
 
-// The two passes over a row's 128 scores. Both are short loops: unrolled, the
-// roles' code together does not stay in the instruction caches (half of the
-// softmax's time went into waiting for instructions). `sc`, in shared memory:
-// ks, vs (scaled by 2^-e) and the four e's, one per 32 tokens.
-
-// Largest score of a row, each plus its e: what the reference follows.
+// A row's scores of a KV tile in the exponent's units (x, -infinity where the
+// row does not see), and the largest, each plus its e: what the reference
+// follows. `sc`, in shared memory: ks, vs (scaled by 2^-e) and the e's, one per
+// 32 tokens. (A tile of 64 also keeps this code, unrolled, short enough for the
+// instruction caches beside that of the other roles; at 128 columns half of the
+// softmax's time went into waiting for instructions.)
 template <bool kMask>
-__device__ __forceinline__ float kv4_row_max(uint32_t s_addr, const float4 *sc, int seen) {
+__device__ __forceinline__ float kv4_row_scores(uint32_t s_addr, const float4 *sc, int seen,
+                                                float2 (&x)[32]) {
   using namespace kv4_prompt_cfg;
+  uint32_t raw[2][32];
+  tmem_ld_x32(s_addr, raw[0]);
+  tmem_ld_x32(s_addr + 32, raw[1]);
+  const float2 e = *reinterpret_cast<const float2 *>(sc + 2 * kTok / 4);
+  tmem_ld_wait(raw[0]);
+  tmem_ld_wait(raw[1]);
   float mx = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t raw[32];
-    tmem_ld_x32(s_addr + 32 * c, raw);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    const float e = reinterpret_cast<const float *>(sc + 2 * kTok / 4)[c];
-    tmem_ld_wait(raw);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float4 k = sc[8 * c + i];
-      float2 x = f2_mul(make_float2(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1])),
-                        make_float2(k.x, k.y));
-      float2 y = f2_mul(make_float2(__uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3])),
-                        make_float2(k.z, k.w));
-      if (kMask) {
-        const int left = seen - 32 * c - 4 * i;
-        if (left <= 0) x.x = -INFINITY;
-        if (left <= 1) x.y = -INFINITY;
-        if (left <= 2) y.x = -INFINITY;
-        if (left <= 3) y.y = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t *r = &raw[c][4 * i + 2 * h];
+        float2 y = f2_mul(make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])),
+                          h == 0 ? make_float2(k.x, k.y) : make_float2(k.z, k.w));
+        if (kMask) {
+          const int left = seen - 32 * c - 4 * i - 2 * h;
+          if (left <= 0) y.x = -INFINITY;
+          if (left <= 1) y.y = -INFINITY;
+        }
+        x[16 * c + 2 * i + h] = y;
+        m4[2 * (i & 1) + h] = fmaxf(m4[2 * (i & 1) + h], fmaxf(y.x, y.y));
       }
-      m4[2 * (i & 1)] = fmaxf(m4[2 * (i & 1)], fmaxf(x.x, x.y));
-      m4[2 * (i & 1) + 1] = fmaxf(m4[2 * (i & 1) + 1], fmaxf(y.x, y.y));
     }
-    mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) + e);
+    mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) + (c == 0 ? e.x : e.y));
   }
   return mx;
 }
 
 // Weights in the reference `top`, times the value scales, as fp16 pairs over the
-// scores (columns 16c .. of W are columns 32c .. of S, which have been read by
-// then). Returns the sum of the weights.
-template <bool kMask>
+// scores; returns their sum.
 __device__ __forceinline__ float kv4_row_weights(uint32_t s_addr, const float4 *sc, float top,
-                                                 int seen) {
+                                                 const float2 (&x)[32]) {
   using namespace kv4_prompt_cfg;
+  const float2 e = *reinterpret_cast<const float2 *>(sc + 2 * kTok / 4);
   float sum = 0.f;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t raw[32], packed[16];
-    tmem_ld_x32(s_addr + 32 * c, raw);
-    const float e = reinterpret_cast<const float *>(sc + 2 * kTok / 4)[c];
-    const float add = e + kRaise - top, back = exp2_approx(-e - kRaise);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const float ec = c == 0 ? e.x : e.y, add = ec + kRaise - top;
     const float2 add2 = make_float2(add, add);
     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    tmem_ld_wait(raw);
+    uint32_t packed[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 k = sc[8 * c + i], v = sc[kTok / 4 + 8 * c + i];
+      const float4 v = sc[kTok / 4 + 8 * c + i];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t *r = &raw[4 * i + 2 * h];
-        float2 y = f2_fma(make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])),
-                          h == 0 ? make_float2(k.x, k.y) : make_float2(k.z, k.w), add2);
+        float2 y = f2_add(x[16 * c + 2 * i + h], add2);
         y.x = exp2_approx(y.x);
         y.y = exp2_approx(y.y);
-        if (kMask) {
-          const int left = seen - 32 * c - 4 * i - 2 * h;
-          if (left <= 0) y.x = 0.f;
-          if (left <= 1) y.y = 0.f;
-        }
         part[h] = f2_add(part[h], y);
         y = f2_mul(y, h == 0 ? make_float2(v.x, v.y) : make_float2(v.z, v.w));
         packed[2 * i + h] = pack_half2_rn(y.x, y.y);
@@ -288,7 +301,7 @@ __device__ __forceinline__ float kv4_row_weights(uint32_t s_addr, const float4 *
     }
     tmem_st_x16(s_addr + 16 * c, packed);
     const float2 both = f2_add(part[0], part[1]);
-    sum = fmaf(both.x + both.y, back, sum);
+    sum = fmaf(both.x + both.y, exp2_approx(-ec - kRaise), sum);
   }
   return sum;
 }
@@ -300,17 +313,17 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem);   // [2] query tile stored
   uint64_t *q_empty = q_full + 2;   // [2] its last product complete
-  uint64_t *s_full = q_empty + 2;   // [2] S of the query tile complete
-  uint64_t *p_full = s_full + 2;    // [2] W stored over S (and O rescaled)
-  uint64_t *o_full = p_full + 2;    // [2] W V complete
-  uint64_t *k_full = o_full + 2;    // [2] key tile expanded
-  uint64_t *k_empty = k_full + 2;   // [2] both products with it complete
-  uint64_t *v_full = k_empty + 2;
-  uint64_t *v_empty = v_full + 2;
-  uint64_t *item_full = v_empty + 2;         // [kItems]
+  uint64_t *s_full = q_empty + 2;   // [2][2] S of the query tile (and buffer) complete
+  uint64_t *p_full = s_full + 4;    // [2][2] W stored over S (and O rescaled)
+  uint64_t *o_full = p_full + 4;    // [2][2] W V complete
+  uint64_t *k_full = o_full + 4;    // [kStages] key tile expanded
+  uint64_t *k_empty = k_full + kStages;   // [kStages] both products with it complete
+  uint64_t *v_full = k_empty + kStages;
+  uint64_t *v_empty = v_full + kStages;
+  uint64_t *item_full = v_empty + kStages;   // [kItems]
   uint64_t *item_empty = item_full + kItems; // [kItems] read by every role
-  uint64_t *done = item_empty + kItems;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  uint64_t *done = item_empty + kItems;      // [2]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   Kv4Item *ring = reinterpret_cast<Kv4Item *>(tmem_slot + 2);   // [kItems]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -319,19 +332,24 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], kQThreads);
       mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&o_full[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
-      mbar_init(&o_full[i], 1);
-      mbar_init(&k_full[i], 128);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 128);
-      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&k_full[i], kTok);
+      mbar_init(&k_empty[i], 2);
+      mbar_init(&v_full[i], kTok);
+      mbar_init(&v_empty[i], 2);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kItemReaders);
     }
-    mbar_init(done, 1);
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -353,16 +371,15 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     report_status(6 /* ATOM_ERR_TIMEOUT */);
     *abort_flag = 1;
   };
-  // The next item for a warp (or a lone thread), in turn; false: a wait gave up.
+  // The next item for a warp, in turn; false: a wait gave up.
   uint32_t item_no = 0;
-  auto take_item = [&](Kv4Item &it, bool whole_warp) -> bool {
+  auto take_item = [&](Kv4Item &it) -> bool {
     const int slot = item_no % kItems;
-    bool ok = mbar_wait_inline(&item_full[slot], (item_no / kItems) & 1, abort_flag);
-    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return false;
+    const bool ok = mbar_wait_inline(&item_full[slot], (item_no / kItems) & 1, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return false;
     it = ring[slot];
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) mbar_arrive(&item_empty[slot]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[slot]);
     ++item_no;
     return true;
   };
@@ -373,13 +390,19 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     const int w = warp >> 2;                     // query tile
     const int tid = threadIdx.x & 127;           // row of it, TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t s_addr = tbase + lane_base + kTmemS + 128 * w;
+    const uint32_t s_base = tbase + lane_base + kTmemS + 128 * w;
     const uint32_t o_addr = tbase + lane_base + kTmemO + 128 * w;
     uint32_t tiles = 0;                          // KV tiles so far, over all items
     bool ok = true;
+    // The output of the no-th tile. (Two barriers, as S has two buffers: the
+    // scores of a tile are complete after the output of the tile two before, so
+    // that a parity names one phase.)
+    auto o_wait = [&](uint32_t no) {
+      return mbar_wait_inline(&o_full[2 * w + (no & 1)], (no >> 1) & 1, abort_flag);
+    };
     for (;;) {
       Kv4Item it;
-      if (!(ok = take_item(it, true)) || !it.more) break;
+      if (!(ok = take_item(it)) || !it.more) break;
       const int r = it.row0 + 128 * w + tid;
       const bool valid = r < it.rows;
       const int qi = valid ? kv4_div(r, p.by_group) : 0;
@@ -390,22 +413,25 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
       const int n = it.kv_tiles;
       float top = kKv4NoMax, sum = 0.f;
       for (int j = 0; j < n; ++j, ++tiles) {
-        ok = mbar_wait_inline(&v_full[tiles & 1], (tiles >> 1) & 1, abort_flag) &&
-             mbar_wait_inline(&s_full[w], tiles & 1, abort_flag);
+        const uint32_t st = tiles % kStages, buf = tiles & 1;
+        const uint32_t s_addr = s_base + 64 * buf;
+        ok = mbar_wait_inline(&v_full[st], (tiles / kStages) & 1, abort_flag) &&
+             mbar_wait_inline(&s_full[2 * w + buf], (tiles >> 1) & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
-        const float4 *sc = reinterpret_cast<const float4 *>(smem + kScOff + (tiles & 3) * kScStage);
+        const float4 *sc = reinterpret_cast<const float4 *>(smem + kScOff + (tiles % kScStages) * kScStage);
         const int seen = limit - j * kTok;   // columns of this tile that the row sees
         const bool mask = __any_sync(0xffffffffu, seen < kTok);
-        const float mx = mask ? kv4_row_max<true>(s_addr, sc, seen)
-                              : kv4_row_max<false>(s_addr, sc, seen);
+        float2 x[32];
+        const float mx = mask ? kv4_row_scores<true>(s_addr, sc, seen, x)
+                              : kv4_row_scores<false>(s_addr, sc, seen, x);
         if (__any_sync(0xffffffffu, mx > top + kLag)) {
           const float up = fmaxf(top, mx);
           const float f = exp2_approx(top - up);
           top = up;
           sum *= f;
           if (j > 0) {   // the output so far, in the new reference
-            ok = mbar_wait_inline(&o_full[w], (tiles - 1) & 1, abort_flag);
+            ok = o_wait(tiles - 1);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after_sync();
 #pragma unroll 1
@@ -419,21 +445,24 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
             }
           }
         }
-        sum += mask ? kv4_row_weights<true>(s_addr, sc, top, seen)
-                    : kv4_row_weights<false>(s_addr, sc, top, seen);
+        sum += kv4_row_weights(s_addr, sc, top, x);
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&p_full[w]);
+        mbar_arrive(&p_full[2 * w + buf]);
       }
       if (!ok) break;
       // ---- the rows' outputs
       const int64_t row = static_cast<int64_t>(it.q0 + qi) * p.q_heads + hq;
       const float inv = sum > 0.f ? __fdiv_rn(exp2_approx(-kRaise), sum) : 0.f;
       if (n > 0) {
-        ok = mbar_wait_inline(&o_full[w], (tiles - 1) & 1, abort_flag);
+        ok = o_wait(tiles - 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
       }
+      // 32 columns at a time through shared memory, so that four lanes write 64
+      // bytes of a row together
+      uint8_t *stage = smem + kOutOff + warp * 2048;
+      const int64_t my_row = valid ? row : -1;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -441,18 +470,26 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
           tmem_ld_x32(o_addr + 32 * c, o);
           tmem_ld_wait(o);
         }
-        if (valid) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {   // 8 columns, in the order 0 4 1 5 2 6 3 7
-            float v[8];
+        for (int i = 0; i < 4; ++i) {   // 8 columns, in the order 0 4 1 5 2 6 3 7
+          float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              v[(k >> 1) + 4 * (k & 1)] = sum > 0.f ? __uint_as_float(o[8 * i + k]) * inv : 0.f;
-            *reinterpret_cast<uint4 *>(p.out + row * 128 + 32 * c + 8 * i) =
-                make_uint4(pack_half2_rn(v[0], v[1]), pack_half2_rn(v[2], v[3]),
-                           pack_half2_rn(v[4], v[5]), pack_half2_rn(v[6], v[7]));
-          }
+          for (int k = 0; k < 8; ++k)
+            v[(k >> 1) + 4 * (k & 1)] = sum > 0.f ? __uint_as_float(o[8 * i + k]) * inv : 0.f;
+          st_shared_v4(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), pack_half2_rn(v[0], v[1]),
+                       pack_half2_rn(v[2], v[3]), pack_half2_rn(v[4], v[5]),
+                       pack_half2_rn(v[6], v[7]));
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int src = 8 * i + (lane >> 2), ch = lane & 3;
+          const int64_t to = __shfl_sync(0xffffffffu, my_row, src);
+          const uint4 v = *reinterpret_cast<const uint4 *>(stage + src * 64 +
+                                                           ((ch ^ ((src >> 1) & 3)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4 *>(p.out + to * 128 + 32 * c + 8 * ch) = v;
+        }
+        __syncwarp();
       }
       if (valid && p.lse != nullptr)
         p.lse[row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945309f : -INFINITY;
@@ -462,8 +499,9 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
   } else if (warp < 16) {
     // ================================================================ expand
     regs_decrease<kExpandRegs>();
-    const bool value = warp >= 12;   // warps 8..11 keys, 12..15 values
-    const int ew = warp & 3, g = lane >> 2, t = lane & 3;
+    const bool value = warp >= 12;   // warps 8..11 keys, 12..15 values;
+    const int turn = (warp >> 1) & 1, ew = warp & 1;   // two warps a tile, in turn
+    const int g = lane >> 2, t = lane & 3;
     const uint8_t *codes = value ? p.v4 : p.k4;
     const float *scales = value ? p.vs : p.ks;
     uint64_t *full = value ? v_full : k_full, *empty = value ? v_empty : k_empty;
@@ -472,7 +510,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     bool ok = true;
     for (;;) {
       Kv4Item it;
-      if (!(ok = take_item(it, true)) || !it.more) break;
+      if (!(ok = take_item(it)) || !it.more) break;
       const int n = it.kv_tiles;
       const int32_t *table = p.seqs.table + it.b * p.seqs.table_stride;
       int page_no = 0, page = -1;      // of the token whose address is made next
@@ -501,18 +539,20 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
           if (v >= 0) q[i] = __ldg(reinterpret_cast<const uint4 *>(codes + v * 64 + t * 16));
         }
       };
-      if (n > 0) {
-        fetch_page(0);
-        load(0);
-        if (n > 1) fetch_page(1);
+      const int first = (turn - tiles) & 1;   // of the item's tiles, for these warps
+      if (first < n) {
+        fetch_page(first);
+        load(first);
+        if (first + 2 < n) fetch_page(first + 2);
       }
-      for (int j = 0; j < n; ++j, ++tiles) {
-        const int st = tiles & 1;
-        ok = mbar_wait_inline(&empty[st], ((tiles >> 1) & 1) ^ 1u, abort_flag);
+      for (int j = first; j < n; j += 2) {
+        const uint32_t no = tiles + j, st = no % kStages;
+        ok = mbar_wait_inline(&empty[st], ((no / kStages) & 1) ^ 1u, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         // scales of this warp's 32 tokens, those of the values divided by 2^e
-        // (the stage of scales was last read four tiles ago)
-        float *sc = reinterpret_cast<float *>(smem + kScOff + (tiles & 3) * kScStage);
+        // (a stage of scales was last read for the tile eight before, whose weights
+        // were complete before the product that freed this operand stage began)
+        float *sc = reinterpret_cast<float *>(smem + kScOff + (no % kScStages) * kScStage);
         if (value) {
           const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(scale));
           int e = static_cast<int>(largest >> 23) - 126;   // every scale < 2^e
@@ -529,27 +569,27 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
           const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 c = codes_f16_chunk(words[k]);
+            const uint4 c = codes_f16_chunk(words[k], !value);
             st_shared_v4(dst + (((4 * (t & 1) + k) ^ (row & 7)) << 4), c.x, c.y, c.z, c.w);
           }
         }
         fence_proxy_async_smem();
         mbar_arrive(&full[st]);
-        if (j + 1 < n) {
-          load(j + 1);
-          if (j + 2 < n) fetch_page(j + 2);
+        if (j + 2 < n) {
+          load(j + 2);
+          if (j + 4 < n) fetch_page(j + 4);
         }
       }
       if (!ok) break;
+      tiles += n;
     }
     if (!ok && lane == 0) fail();
   } else {
     regs_decrease<kOtherRegs>();
-    if (warp > kMmaWarp) {
+    if (warp >= kQWarp) {
       // ============================================================== queries
-      // Finds the items (first warp, one thread) and stores their query rows in
-      // the order of the codes, as soon as the tile's last product with the
-      // previous ones is complete.
+      // Finds the items (one thread) and copies their query rows, each tile as
+      // soon as the last product with the previous one is complete.
       int b = line.b, turn = 0;
       int64_t place = blockIdx.x, rest = line.rest;
       uint32_t loads = 0, made = 0;
@@ -570,41 +610,31 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
         return true;
       };
       bool ok = true;
-      const int qt = threadIdx.x - 32 * (kMmaWarp + 1);   // 0 .. kQThreads - 1
+      const int qt = threadIdx.x - 32 * kQWarp;   // 0 .. kQThreads - 1
       if (qt == 0) ok = make_item();
       for (;;) {
         // one item ahead, so that no role waits for the search
         if (qt == 0 && ok && ring[(made - 1) % kItems].more) ok = make_item();
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         Kv4Item it;
-        if (!(ok = take_item(it, true)) || !it.more) break;
+        if (!(ok = take_item(it)) || !it.more) break;
         if (it.kv_tiles == 0) continue;
         for (int w = 0; w < 2; ++w) {
           ok = mbar_wait_inline(&q_empty[w], (loads & 1) ^ 1u, abort_flag);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           // 16 lanes a row, a 16-byte chunk each
-          for (int i0 = qt; i0 < 128 * 16; i0 += 8 * kQThreads) {
-            uint4 x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int i = i0 + u * kQThreads, r = it.row0 + 128 * w + (i >> 4);
-              x[u] = make_uint4(0u, 0u, 0u, 0u);
-              if (i < 128 * 16 && r < it.rows) {
-                const int qi = kv4_div(r, p.by_group), hq = it.head * p.group + r - qi * p.group;
-                x[u] = __ldg(reinterpret_cast<const uint4 *>(p.q + (it.q0 + qi) * p.q_token +
-                                                             hq * p.q_head) + (i & 15));
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int i = i0 + u * kQThreads, row = i >> 4, c = i & 15;
-              if (i < 128 * 16)
-                st_shared_v4(smem + kQOff + w * kTile + (c >> 3) * kHalf + row * 128 +
-                                 (((c & 7) ^ (row & 7)) << 4),
-                             __byte_perm(x[u].x, x[u].z, 0x5410), __byte_perm(x[u].x, x[u].z, 0x7632),
-                             __byte_perm(x[u].y, x[u].w, 0x5410), __byte_perm(x[u].y, x[u].w, 0x7632));
-            }
+          const uint32_t tile = smem_addr(smem + kQOff + w * kQTile);
+#pragma unroll 4
+          for (int i = qt; i < 128 * 16; i += kQThreads) {
+            const int row = i >> 4, c = i & 15, r = it.row0 + 128 * w + row;
+            const bool valid = r < it.rows;
+            const int qi = valid ? kv4_div(r, p.by_group) : 0;
+            const int hq = it.head * p.group + (valid ? r - qi * p.group : 0);
+            cp_async_16(tile + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                        p.q + (it.q0 + qi) * p.q_token + hq * p.q_head + 8 * c, valid ? 16u : 0u);
           }
+          cp_async_commit();
+          cp_async_wait<0>();
           fence_proxy_async_smem();
           mbar_arrive(&q_full[w]);
         }
@@ -612,69 +642,69 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
         ++loads;
       }
       if (!ok && lane == 0) fail();
-    } else if (lane == 0) {
+    } else {
       // ============================================================== MMA issuer
       uint32_t tiles = 0, items = 0;
       bool ok = true;
       const uint32_t q_lo = desc_lo_k(smem_addr(smem + kQOff));
       const uint32_t k_lo = desc_lo_k(smem_addr(smem + kKOff));
       const uint32_t v_lo = desc_lo_mn(smem_addr(smem + kVOff), kHalf);
-      auto scores = [&](int w, int st, bool last) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-          mma_f16_ss(tbase + kTmemS + 128 * w, q_lo + w * (kTile >> 4) + off,
-                     k_lo + st * (kTile >> 4) + off, kIdescS, k > 0 ? 1u : 0u);
-        }
-        tc_commit(&s_full[w]);
-        if (last) tc_commit(&q_empty[w]);
-        if (w == 1) tc_commit(&k_empty[st]);
-      };
-      auto outputs = [&](int w, int st, bool first) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_f16_ts(tbase + kTmemO + 128 * w, tbase + kTmemS + 128 * w + 8 * k,
-                     v_lo + st * (kTile >> 4) + k * (2048 >> 4), kIdescO,
-                     !first || k > 0 ? 1u : 0u);
-        tc_commit(&o_full[w]);
-        if (w == 1) tc_commit(&v_empty[st]);
-      };
+      // The warp stays together and one lane issues: the operands' descriptors
+      // are then known to be the same for the whole warp.
+      const bool leader = elect_one();
+      const int w = warp - kMmaWarp;
+      const uint32_t s_tmem = tbase + kTmemS + 128 * w, o_tmem = tbase + kTmemO + 128 * w;
       for (;;) {
         Kv4Item it;
-        if (!(ok = take_item(it, false)) || !it.more) break;
+        if (!(ok = take_item(it)) || !it.more) break;
         const int n = it.kv_tiles;
         if (n == 0) continue;
-        // step j: W V of tile j - 1, then Q K^T of tile j, for one query tile
-        // and then the other
-        for (int j = 0; ok && j <= n; ++j) {
-          const int st = tiles & 1, pst = (tiles - 1) & 1;
-#pragma unroll 1
-          for (int w = 0; w < 2; ++w) {
-            if (j > 0) {
-              ok = (w != 0 || mbar_wait(&v_full[pst], ((tiles - 1) >> 1) & 1, abort_flag)) &&
-                   mbar_wait(&p_full[w], (tiles - 1) & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after_sync();
-              outputs(w, pst, j == 1);
-            } else {
-              ok = mbar_wait(&q_full[w], items & 1, abort_flag);
-              if (!ok) break;
+        ok = mbar_wait(&q_full[w], items & 1, abort_flag);
+        // step j: the output of tile j - 2, when its weights are there, then S of
+        // tile j in the buffer that they leave
+        for (int j = 0; ok && j < n + 2; ++j) {
+          const uint32_t no = tiles + j, st = no % kStages, s_buf = s_tmem + 64 * (no & 1);
+          if (j >= 2) {
+            const uint32_t old = no - 2, ost = old % kStages;
+            ok = mbar_wait(&v_full[ost], (old / kStages) & 1, abort_flag) &&
+                 mbar_wait(&p_full[2 * w + (old & 1)], (old >> 1) & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after_sync();
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < kTok / 16; ++k)
+                mma_f16_ts(o_tmem, s_buf + 8 * k, v_lo + ((ost * kTile + k * 2048) >> 4), kIdescO,
+                           j > 2 || k > 0 ? 1u : 0u);
+              tc_commit(&o_full[2 * w + (old & 1)]);
+              tc_commit(&v_empty[ost]);
             }
-            if (j < n) {
-              if (w == 0 && !(ok = mbar_wait(&k_full[st], (tiles >> 1) & 1, abort_flag))) break;
-              tc_fence_after_sync();
-              scores(w, st, j + 1 == n);
-            }
+            __syncwarp();
           }
-          if (j < n) ++tiles;
+          if (j < n) {
+            ok = mbar_wait(&k_full[st], (no / kStages) & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after_sync();
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_f16_ss(s_buf, q_lo + ((w * kQTile + (k >> 2) * kQHalf + (k & 3) * 32) >> 4),
+                           k_lo + ((st * kTile + (k >> 2) * kHalf + (k & 3) * 32) >> 4), kIdescS,
+                           k > 0 ? 1u : 0u);
+              tc_commit(&s_full[2 * w + (no & 1)]);
+              tc_commit(&k_empty[st]);
+              if (j + 1 == n) tc_commit(&q_empty[w]);
+            }
+            __syncwarp();
+          }
         }
         if (!ok) break;
+        tiles += n;
         ++items;
       }
-      if (!ok) fail();
+      if (!ok && lane == 0) fail();
       // nothing may still write TMEM or read shared memory when they are released
-      tc_commit(done);
-      (void)mbar_wait(done, 0, nullptr);
+      if (leader) tc_commit(&done[w]);
+      (void)mbar_wait(&done[w], 0, nullptr);
     }
     __syncwarp();
   }
