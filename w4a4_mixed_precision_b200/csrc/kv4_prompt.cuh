@@ -19,12 +19,12 @@
 // The range of W. vs spans what the values spanned, so the scales of each 32
 // tokens are divided by 2^e, e the exponent of their maximum, and a row's
 // reference R is the running maximum of (its largest x among them) + e: W is
-// then at most 2^15 (R lags by up to 8 before the output is rescaled, W is
-// raised by 2^7) whatever the scales are, and W keeps fp16's full precision
-// down to 2^-21 of R's own, and an absolute error of 2^-32 of the tokens'
-// largest value below. The sum of weights uses the same reference. (A lag of 4
-// made two warps in five rescale on every tile of the 4096-token prompt: one
-// row of 32 is enough.)
+// then at most 2^15 (R lags by up to 11 before the output is rescaled, W is
+// raised by 2^4) whatever the scales are, and W keeps fp16's full precision down
+// to 2^-18 of R's own, and an absolute error of 2^-29 of the tokens' largest
+// value below. The sum of weights uses the same reference. (One row of 32 that
+// outgrows R costs its warp the wait for the output so far: with a lag of 4 two
+// warps in five did so in every tile of the 4096-token prompt, with 8 one in ten.)
 //
 // Roles (640 threads, one CTA per SM, a persistent loop over the work):
 //   warps 0..3, 4..7     softmax of query tile 0 and 1: thread = row = TMEM lane
@@ -72,7 +72,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;       // + 128 * query tile; S + 64 * (tile & 1)
 constexpr uint32_t kIdescS = idesc_f16(128, kTok);
 constexpr uint32_t kIdescO = idesc_f16(128, 128) | (1u << 16);   // B is MN-major
-constexpr float kRaise = 7.f, kLag = 8.f;
+constexpr float kRaise = 4.f, kLag = 11.f;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 }  // namespace kv4_prompt_cfg
 
@@ -124,6 +124,19 @@ __device__ __forceinline__ uint32_t desc_lo_k(uint32_t saddr) {
 }
 __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t lbo) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+
+// Bounded wait that leaves the issue slots to the other warps: a first look,
+// then one every `ns` nanoseconds or so.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity,
+                                               const volatile int *abort_flag, uint32_t ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 0; i < kWaitLimitNs / 32; ++i) {
+    __nanosleep(ns);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  return false;
 }
 
 // True in one lane of the (converged) warp.
@@ -231,6 +244,12 @@ __device__ __forceinline__ Kv4Item kv4_prompt_item(const Kv4Attn &p, int &b, int
   return it;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // A row's scores of a KV tile in the exponent's units (x, -infinity where the
 // row does not see), and the largest, each plus its e: what the reference
 // follows. `sc`, in shared memory: ks, vs (scaled by 2^-e) and the e's, one per
@@ -265,7 +284,7 @@ __device__ __forceinline__ float kv4_row_scores(uint32_t s_addr, const float4 *s
           if (left <= 1) y.y = -INFINITY;
         }
         x[16 * c + 2 * i + h] = y;
-        m4[2 * (i & 1) + h] = fmaxf(m4[2 * (i & 1) + h], fmaxf(y.x, y.y));
+        m4[2 * (i & 1) + h] = max3(m4[2 * (i & 1) + h], y.x, y.y);
       }
     }
     mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) + (c == 0 ? e.x : e.y));
@@ -330,18 +349,18 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], kQThreads);
+      mbar_init(&q_full[i], kQThreads / 32);
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&o_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);   // one arrival per warp, here and below
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&k_full[i], kTok);
+      mbar_init(&k_full[i], 2);
       mbar_init(&k_empty[i], 2);
-      mbar_init(&v_full[i], kTok);
+      mbar_init(&v_full[i], 2);
       mbar_init(&v_empty[i], 2);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -375,7 +394,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
   uint32_t item_no = 0;
   auto take_item = [&](Kv4Item &it) -> bool {
     const int slot = item_no % kItems;
-    const bool ok = mbar_wait_inline(&item_full[slot], (item_no / kItems) & 1, abort_flag);
+    const bool ok = mbar_wait_idle(&item_full[slot], (item_no / kItems) & 1, abort_flag, 64);
     if (!__all_sync(0xffffffffu, ok)) return false;
     it = ring[slot];
     __syncwarp();
@@ -413,10 +432,8 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
       const int n = it.kv_tiles;
       float top = kKv4NoMax, sum = 0.f;
       for (int j = 0; j < n; ++j, ++tiles) {
-        const uint32_t st = tiles % kStages, buf = tiles & 1;
-        const uint32_t s_addr = s_base + 64 * buf;
-        ok = mbar_wait_inline(&v_full[st], (tiles / kStages) & 1, abort_flag) &&
-             mbar_wait_inline(&s_full[2 * w + buf], (tiles >> 1) & 1, abort_flag);
+        const uint32_t buf = tiles & 1, s_addr = s_base + 64 * buf;
+        ok = mbar_wait_inline(&s_full[2 * w + buf], (tiles >> 1) & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
         const float4 *sc = reinterpret_cast<const float4 *>(smem + kScOff + (tiles % kScStages) * kScStage);
@@ -448,7 +465,8 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
         sum += kv4_row_weights(s_addr, sc, top, x);
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&p_full[2 * w + buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * w + buf]);
       }
       if (!ok) break;
       // ---- the rows' outputs
@@ -547,7 +565,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
       }
       for (int j = first; j < n; j += 2) {
         const uint32_t no = tiles + j, st = no % kStages;
-        ok = mbar_wait_inline(&empty[st], ((no / kStages) & 1) ^ 1u, abort_flag);
+        ok = mbar_wait_idle(&empty[st], ((no / kStages) & 1) ^ 1u, abort_flag, 64);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         // scales of this warp's 32 tokens, those of the values divided by 2^e
         // (a stage of scales was last read for the tile eight before, whose weights
@@ -574,7 +592,8 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&full[st]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
         if (j + 2 < n) {
           load(j + 2);
           if (j + 4 < n) fetch_page(j + 4);
@@ -595,7 +614,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
       uint32_t loads = 0, made = 0;
       auto make_item = [&]() -> bool {   // one thread
         const int slot = made % kItems;
-        if (!mbar_wait_inline(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag)) return false;
+        if (!mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64)) return false;
         Kv4Item it{};
         if (place < line.total) {
           it = kv4_prompt_item(p, b, rest);
@@ -620,7 +639,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
         if (!(ok = take_item(it)) || !it.more) break;
         if (it.kv_tiles == 0) continue;
         for (int w = 0; w < 2; ++w) {
-          ok = mbar_wait_inline(&q_empty[w], (loads & 1) ^ 1u, abort_flag);
+          ok = mbar_wait_idle(&q_empty[w], (loads & 1) ^ 1u, abort_flag, 128);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
           // 16 lanes a row, a 16-byte chunk each
           const uint32_t tile = smem_addr(smem + kQOff + w * kQTile);
@@ -636,7 +655,8 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
           cp_async_commit();
           cp_async_wait<0>();
           fence_proxy_async_smem();
-          mbar_arrive(&q_full[w]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[w]);
         }
         if (!ok) break;
         ++loads;
@@ -666,8 +686,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
           const uint32_t no = tiles + j, st = no % kStages, s_buf = s_tmem + 64 * (no & 1);
           if (j >= 2) {
             const uint32_t old = no - 2, ost = old % kStages;
-            ok = mbar_wait(&v_full[ost], (old / kStages) & 1, abort_flag) &&
-                 mbar_wait(&p_full[2 * w + (old & 1)], (old >> 1) & 1, abort_flag);
+            ok = mbar_wait(&p_full[2 * w + (old & 1)], (old >> 1) & 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after_sync();
             if (leader) {
@@ -681,7 +700,9 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
             __syncwarp();
           }
           if (j < n) {
-            ok = mbar_wait(&k_full[st], (no / kStages) & 1, abort_flag);
+            // (the values' scales are needed as soon as the scores are there)
+            ok = mbar_wait(&k_full[st], (no / kStages) & 1, abort_flag) &&
+                 mbar_wait(&v_full[st], (no / kStages) & 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after_sync();
             if (leader) {
