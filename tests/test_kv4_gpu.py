@@ -114,6 +114,9 @@ def test_empty_sequences_and_rows(token_major):
     ([130, 1, 257], [400, 900, 257], 4, 2),
     ([300], [300], 8, 1),
     ([1], [1], 40, 1),
+    ([3, 70], [30, 200], 130, 1),
+    ([2, 3], [30, 200], 128, 1),
+    ([50], [60], 96, 2),
     ([17, 0, 1, 300, 40], [17, 30, 0, 777, 20], 4, 4),
     ([1000], [1100], 7, 1),
     ([129, 128, 127, 33], [129, 4096, 128, 1500], 16, 8),
@@ -200,6 +203,10 @@ def test_scale_and_larger_bound_on_new_tokens():
     ([64, 100], [64, 500], 4, 4, 7),
     ([200], [200], 16, 2, 64),
     ([1, 4], [0, 2], 4, 2, 16),
+    ([40, 3, 0, 130], [40, 90, 20, 700], 4, 4, 24),
+    ([1000], [1300], 7, 1, 100),
+    ([257, 300], [257, 129], 8, 8, 16),
+    ([513], [2000], 16, 4, 64),
 ])
 def test_attention_weights(new, lens, q_heads, heads, page, causal):
     c = Call(21, new, lens, q_heads=q_heads, heads=heads, page=page, q_size=0.05)

@@ -144,9 +144,9 @@ atom_status_t kv4_decode_ctas(DeviceState *dev, int nt, int *ctas) {
 
 // Launch that may overlap the end of the kernel before it in the stream (the
 // kernel waits for that one before it touches memory).
-template <class P>
-cudaError_t kv4_launch(void (*fn)(const P), int grid, int threads, size_t smem,
-                       atom_stream_t stream, const P &p) {
+template <class... P>
+cudaError_t kv4_launch(void (*fn)(P...), int grid, int threads, size_t smem,
+                       atom_stream_t stream, const P &...p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -157,7 +157,33 @@ cudaError_t kv4_launch(void (*fn)(const P), int grid, int threads, size_t smem,
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, p);
+  return cudaLaunchKernelEx(&cfg, fn, p...);
+}
+
+// Tensor map of fp16 queries [rows][q_heads][128] whose boxes are the rows of as
+// many whole tokens of a KV head as make at most 128, half a vector wide.
+bool kv4_query_map(CUtensorMap *map, const void *q, int64_t q_token, int64_t q_head, int64_t rows,
+                   int64_t q_heads, int group) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  // (a dimension of one has no stride of its own)
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(q_heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(q_heads > 1 ? q_head * 2 : 256),
+                                 static_cast<cuuint64_t>(rows > 1 ? q_token * 2 : 256)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether the prompt kernels can take a call: its longest sequence has more rows
+// than the decode kernel should take, its tokens' rows fit a tile, and a tensor
+// map describes its queries.
+bool kv4_prompt_call(CUtensorMap *map, const void *q, int64_t q_token, int64_t q_head, int64_t rows,
+                     int64_t q_heads, int group, int64_t max_q) {
+  return max_q * group > kKv4FewRows && group <= 128 &&
+         kv4_query_map(map, q, q_token, q_head, rows, q_heads, group);
 }
 
 constexpr float kLog2e = 1.44269504088896341f;
@@ -239,8 +265,11 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   p.max_q = static_cast<int>(batch->max_q < rows ? batch->max_q : rows);
   // Sequences with up to 16 query rows a KV head go to the decode kernel, those
   // with more to the prompt kernel; one that no sequence can need is not launched.
-  const int64_t most_rows = static_cast<int64_t>(p.max_q) * p.group;
-  const bool prompts = most_rows > kKv4FewRows, decode = !prompts || batch->batch > 1;
+  CUtensorMap q_map;
+  const bool prompts =
+      kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, p.max_q);
+  const bool decode = !prompts || batch->batch > 1;
+  p.tile_rows = prompts ? 128 / p.group * p.group : 0;
   p.few_rows = !prompts ? INT32_MAX : (decode ? kKv4FewRows : 0);
   cudaError_t err = cudaSuccess;
   if (prompts) {
@@ -251,7 +280,7 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
         return ATOM_ERR_CUDA;
       dev->kv4_prompt_attr.store(true, std::memory_order_release);
     }
-    err = kv4_launch(atomk::kv4_prompt_kernel, dev->sm_count, kThreads, kSmemBytes, stream, p);
+    err = kv4_launch(atomk::kv4_prompt_kernel, dev->sm_count, kThreads, kSmemBytes, stream, q_map, p);
   }
   if (err == cudaSuccess && decode) {
     using namespace atomk::kv4_decode_cfg;
@@ -300,11 +329,34 @@ atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t
   p.group = static_cast<int>(q_heads / cache->heads);
   p.scale_log2 = scale * kLog2e;
   p.causal = causal != 0 ? 1 : 0;
+  p.by_group = atomk::kv4_div_by(p.group);
   p.prev = prev;
   p.sums = sums;
   p.width = width;
-  const cudaError_t err = kv4_launch(atomk::kv4_weights_kernel, 4 * dev->sm_count,
-                                     atomk::kKv4WeightThreads, 0, stream, p);
+  // as in atom_kv4_attention (a larger sequence than max_q says costs time here,
+  // nothing else)
+  const int64_t max_q = batch->max_q < rows ? batch->max_q : rows;
+  CUtensorMap q_map;
+  const bool prompts = kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, max_q);
+  const bool few = !prompts || batch->batch > 1;
+  p.tile_rows = prompts ? 128 / p.group * p.group : 0;
+  p.few_rows = !prompts ? INT32_MAX : (few ? kKv4FewRows : 0);
+  cudaError_t err = cudaSuccess;
+  if (prompts) {
+    using namespace atomk::kv4_wprompt_cfg;
+    if (!dev->kv4_wprompt_attr.load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(atomk::kv4_weights_prompt_kernel,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kSmemBytes)) != cudaSuccess)
+        return ATOM_ERR_CUDA;
+      dev->kv4_wprompt_attr.store(true, std::memory_order_release);
+    }
+    err = kv4_launch(atomk::kv4_weights_prompt_kernel, dev->sm_count, kThreads, kSmemBytes, stream,
+                     q_map, p);
+  }
+  if (err == cudaSuccess && few)
+    err = kv4_launch(atomk::kv4_weights_kernel, 4 * dev->sm_count, atomk::kKv4WeightThreads, 0,
+                     stream, p);
   return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 

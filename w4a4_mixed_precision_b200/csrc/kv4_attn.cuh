@@ -53,6 +53,7 @@ struct Kv4Attn {
   Kv4Seqs seqs;
   int q_heads, group;
   Kv4Div by_group;
+  int tile_rows;                // query rows of a prompt tile: whole tokens' rows, up to 128
   float scale_log2;             // scale * log2(e)
   int causal;
   int max_q;                    // largest qn of the call, as its caller says

@@ -2,7 +2,8 @@
 // prompts) over the paged INT4 KV cache, on the tcgen05 tensor cores. The
 // formulas are kv4_attn.cuh's.
 //
-// A CTA takes 256 query rows of a (sequence, KV head) as two tiles of 128, and
+// A CTA takes up to 256 query rows of a (sequence, KV head) as two tiles of 128
+// (of as many whole tokens' rows as fit: a tile is one box of a tensor copy), and
 // the cached tokens that they see in tiles of 64. Per KV tile and query tile:
 //   S = Q K^T     128x64x128, fp16 codes of K from shared memory, fp32 S in TMEM
 //   W = 2^(x - R) * vs, x = S * ks * scale * log2(e)   (one thread a row; fp16, into TMEM
@@ -30,7 +31,7 @@
 //   warps 0..3, 4..7     softmax of query tile 0 and 1: thread = row = TMEM lane
 //   warps 8..11, 12..15  load packed keys and values, expand them to operand tiles
 //   warps 16, 17         issue the MMAs of query tile 0 and 1
-//   warps 18, 19         find the work items, copy their queries
+//   warp 18, lane 0      finds the work items, starts the copies of their queries
 // While the tensor core multiplies for one query tile, the other tile's
 // weights are made. What bounds it: the exponentials, 16 per clock and SM (1024
 // clocks per 128x128 tile), as much as the two products (1024 clocks).
@@ -49,13 +50,11 @@ namespace atomk {
 namespace kv4_prompt_cfg {
 constexpr int kThreads = 640;
 constexpr int kMmaWarp = 16;         // and 17: one for each query tile
-constexpr int kQWarp = 18;           // and 19
-constexpr int kQThreads = 64;
+constexpr int kQWarp = 18;
 constexpr int kItems = 4;            // ring of work items
-constexpr int kItemReaders = 8 + 8 + 2 + 2;   // softmax, expanding, MMA, query warps
+constexpr int kItemReaders = 8 + 8 + 2 + 1;   // softmax, expanding, MMA warps, queries
 // registers: 144 * 256 + 64 * 256 + 64 * 128 = 96 * 640, what the launch has
 constexpr int kSoftRegs = 144, kExpandRegs = 64, kOtherRegs = 64;
-constexpr int kRows = 256;           // query rows of a CTA's work item
 constexpr int kTok = 64;             // tokens of a KV tile
 constexpr int kStages = 4;           // of key and of value tiles
 constexpr int kScStages = 8;         // of their scales
@@ -199,11 +198,11 @@ __device__ __forceinline__ uint4 codes_f16_chunk(uint32_t w, bool in_order) {
                     __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
 }
 
-// The items of the persistent loop: query tiles of kRows rows in the order
-// sequence, tile (the last, which sees most, first), head. Of each `grid` places
-// in turn CTA i takes the i-th, of every second turn the i-th from the end, so
-// that large and small items meet in a CTA. One thread finds them and hands them
-// on through a ring in shared memory.
+// The items of the persistent loop: pairs of query tiles in the order sequence,
+// pair (the last, which sees most, first), head. Of each `grid` places in turn
+// CTA i takes the i-th, of every second turn the i-th from the end, so that
+// large and small items meet in a CTA. One thread finds them and hands them on
+// through a ring in shared memory.
 struct Kv4Item {
   int b, head, row0, rows;   // rows: query rows of the sequence and head
   int kv_tiles, last;        // KV tiles and cached positions that the tile's rows see
@@ -212,7 +211,7 @@ struct Kv4Item {
 
 __device__ __forceinline__ int64_t kv4_prompt_weight(const Kv4Seq &s, const Kv4Attn &p) {
   if (kv4_too_many(s, p) || static_cast<int64_t>(s.qn) * p.group <= p.few_rows) return 0;
-  return static_cast<int64_t>(kv4_tiles(s, p.group, kv4_prompt_cfg::kRows)) * p.geom.heads;
+  return static_cast<int64_t>(kv4_tiles(s, p.group, 2 * p.tile_rows)) * p.geom.heads;
 }
 
 // The item `rest` places into sequence b; both move on to the sequence that
@@ -230,11 +229,11 @@ __device__ __forceinline__ Kv4Item kv4_prompt_item(const Kv4Attn &p, int &b, int
   Kv4Item it;
   it.b = b;
   it.rows = s.qn * p.group;
-  const int tiles = kv4_tiles(s, p.group, kRows);
+  const int item_rows = 2 * p.tile_rows, tiles = kv4_tiles(s, p.group, item_rows);
   const int at = static_cast<int>(rest / p.geom.heads);
   it.head = static_cast<int>(rest - static_cast<int64_t>(at) * p.geom.heads);
-  it.row0 = (tiles - 1 - at) * kRows;
-  const int last_row = (it.rows - it.row0 > kRows ? it.row0 + kRows : it.rows) - 1;
+  it.row0 = (tiles - 1 - at) * item_rows;
+  const int last_row = (it.rows - it.row0 > item_rows ? it.row0 + item_rows : it.rows) - 1;
   it.last = kv4_limit(s, last_row / p.group, p.causal != 0);
   it.kv_tiles = (it.last + kTok - 1) / kTok;
   it.q0 = s.q0;
@@ -326,7 +325,7 @@ __device__ __forceinline__ float kv4_row_weights(uint32_t s_addr, const float4 *
 }
 
 __global__ void __launch_bounds__(kv4_prompt_cfg::kThreads, 1)
-kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
+kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ Kv4Attn p) {
   using namespace kv4_prompt_cfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -349,7 +348,7 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], kQThreads / 32);
+      mbar_init(&q_full[i], 1);     // + the copies' bytes
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -376,6 +375,10 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  // rows of the query tiles that no copy reaches
+  for (uint32_t i = threadIdx.x; i < 2 * kQTile / 16; i += kThreads)
+    st_shared_v4(smem + kQOff + 16 * i, 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   grid_dependency_wait();
   const Kv4Line line = kv4_find_place<kThreads / 32>(
       p.seqs, [&](const Kv4Seq &s) { return kv4_prompt_weight(s, p); },
@@ -422,11 +425,12 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     for (;;) {
       Kv4Item it;
       if (!(ok = take_item(it)) || !it.more) break;
-      const int r = it.row0 + 128 * w + tid;
-      const bool valid = r < it.rows;
+      const int r = it.row0 + p.tile_rows * w + tid;
+      const bool valid = tid < p.tile_rows && r < it.rows;
       const int qi = valid ? kv4_div(r, p.by_group) : 0;
       const int hq = it.head * p.group + (valid ? r - qi * p.group : 0);
-      // (a row past the last computes on zeros and is not written)
+      // (a row that is none computes on what the copy brought, or on the zeros
+      // that the tile began with, and is not written)
       const int limit =
           valid ? kv4_limit(Kv4Seq{it.q0, it.qn, it.len, true}, qi, p.causal != 0) : INT32_MAX;
       const int n = it.kv_tiles;
@@ -607,61 +611,49 @@ kv4_prompt_kernel(const __grid_constant__ Kv4Attn p) {
     regs_decrease<kOtherRegs>();
     if (warp >= kQWarp) {
       // ============================================================== queries
-      // Finds the items (one thread) and copies their query rows, each tile as
-      // soon as the last product with the previous one is complete.
-      int b = line.b, turn = 0;
-      int64_t place = blockIdx.x, rest = line.rest;
-      uint32_t loads = 0, made = 0;
-      auto make_item = [&]() -> bool {   // one thread
-        const int slot = made % kItems;
-        if (!mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64)) return false;
-        Kv4Item it{};
-        if (place < line.total) {
-          it = kv4_prompt_item(p, b, rest);
-          const int grid = static_cast<int>(gridDim.x), i = static_cast<int>(blockIdx.x);
-          const int step = ++turn & 1 ? 2 * (grid - 1 - i) + 1 : 2 * i + 1;
-          place += step;
-          rest += step;
-        }
-        ring[slot] = it;
-        mbar_arrive(&item_full[slot]);
-        ++made;
-        return true;
-      };
-      bool ok = true;
-      const int qt = threadIdx.x - 32 * kQWarp;   // 0 .. kQThreads - 1
-      if (qt == 0) ok = make_item();
-      for (;;) {
-        // one item ahead, so that no role waits for the search
-        if (qt == 0 && ok && ring[(made - 1) % kItems].more) ok = make_item();
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        Kv4Item it;
-        if (!(ok = take_item(it)) || !it.more) break;
-        if (it.kv_tiles == 0) continue;
-        for (int w = 0; w < 2; ++w) {
-          ok = mbar_wait_idle(&q_empty[w], (loads & 1) ^ 1u, abort_flag, 128);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          // 16 lanes a row, a 16-byte chunk each
-          const uint32_t tile = smem_addr(smem + kQOff + w * kQTile);
-#pragma unroll 4
-          for (int i = qt; i < 128 * 16; i += kQThreads) {
-            const int row = i >> 4, c = i & 15, r = it.row0 + 128 * w + row;
-            const bool valid = r < it.rows;
-            const int qi = valid ? kv4_div(r, p.by_group) : 0;
-            const int hq = it.head * p.group + (valid ? r - qi * p.group : 0);
-            cp_async_16(tile + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                        p.q + (it.q0 + qi) * p.q_token + hq * p.q_head + 8 * c, valid ? 16u : 0u);
+      // Finds the items and starts the copy of each query tile as soon as the
+      // last product with the previous one is complete.
+      if (warp == kQWarp && lane == 0) {
+        int b = line.b, turn = 0;
+        int64_t place = blockIdx.x, rest = line.rest;
+        uint32_t loads = 0;
+        bool ok = true;
+        const uint32_t bytes = p.tile_rows * 256;
+        for (uint32_t made = 0;; ++made) {
+          const int slot = made % kItems;
+          if (!(ok = mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64)))
+            break;
+          Kv4Item it{};
+          if (place < line.total) {
+            it = kv4_prompt_item(p, b, rest);
+            const int grid = static_cast<int>(gridDim.x), i = static_cast<int>(blockIdx.x);
+            const int step = ++turn & 1 ? 2 * (grid - 1 - i) + 1 : 2 * i + 1;
+            place += step;
+            rest += step;
           }
-          cp_async_commit();
-          cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&q_full[w]);
+          ring[slot] = it;
+          mbar_arrive(&item_full[slot]);
+          mbar_arrive(&item_empty[slot]);   // as one of its readers
+          if (!it.more) break;
+          if (it.kv_tiles == 0) continue;
+          for (int w = 0; w < 2; ++w) {
+            if (!(ok = mbar_wait_idle(&q_empty[w], (loads & 1) ^ 1u, abort_flag, 32))) break;
+            mbar_arrive_expect_tx(&q_full[w], bytes);
+            const int tok = it.q0 + kv4_div(it.row0 + p.tile_rows * w, p.by_group);
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(smem + kQOff + w * kQTile + h * kQHalf, &q_map, 64 * h, it.head * p.group,
+                          tok, &q_full[w]);
+          }
+          if (!ok) break;
+          ++loads;
         }
-        if (!ok) break;
-        ++loads;
+        if (!ok) {
+          fail();
+          // copies in flight land before shared memory is released
+          for (int w = 0; w < 2; ++w)
+            if (loads > 0) (void)mbar_wait(&q_full[w], (loads - 1) & 1, nullptr);
+        }
       }
-      if (!ok && lane == 0) fail();
     } else {
       // ============================================================== MMA issuer
       uint32_t tiles = 0, items = 0;

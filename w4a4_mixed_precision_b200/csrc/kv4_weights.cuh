@@ -4,12 +4,24 @@
 //                   the query heads of KV head h of exp(s[i][t] - lse[i])
 //
 // with the scores s of kv4_attn.cuh and the log-sum-exps that the attention
-// returned. Only keys are read. A warp holds the key fragments of 32 tokens and
-// passes all query rows that see one of them by, 8 at a time, so every sum is
-// made by one warp in a fixed order: no atomics, the same result every time.
+// returned. Only keys are read. Every sum is made in a fixed order: no atomics,
+// the same result every time.
+//
+// Few query rows (single and drafted tokens), kv4_weights_kernel: a warp holds
+// the key fragments of 32 tokens and passes the query rows that see one of them
+// by, 8 at a time.
+//
+// Many (prompts), kv4_weights_prompt_kernel: the transposed product K Q^T on the
+// tcgen05 tensor cores. A CTA takes 128 tokens of a (sequence, KV head) and all
+// query rows that see one of them in tiles of 128. A token is a row of the
+// product, that is a TMEM lane and a thread: its scale is one register, its sum
+// another, and nothing is reduced across threads. The expanded keys stay in TMEM
+// as the A operand (read from shared memory for each product, A costs 105
+// cycles a 128x128x16 MMA instead of 74). What bounds it: the exponentials, 1024
+// cycles of the SM per 128x128 tile, against 592 of the tensor core.
 #pragma once
 
-#include "kv4_attn.cuh"
+#include "kv4_prompt.cuh"
 
 namespace atomk {
 
@@ -22,8 +34,12 @@ struct Kv4Weights {
   Kv4Geom geom;
   Kv4Seqs seqs;
   int q_heads, group;
+  Kv4Div by_group;
+  int tile_rows;         // query rows of a tile: whole tokens' rows, up to 128
   float scale_log2;
   int causal;
+  int few_rows;          // sequences of up to so many rows a KV head go to the first
+                         // kernel, the others to the second
   const float *prev;     // [batch][heads][width], or null
   float *sums;           // [batch][heads][width]
   int64_t width;
@@ -36,7 +52,9 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
   constexpr int kWarps = kKv4WeightThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   grid_dependency_wait();
-  auto units_of = [&](const Kv4Seq &s) { return s.len > 0 ? kv4_units(s.len) : 0; };
+  auto units_of = [&](const Kv4Seq &s) {
+    return s.len > 0 && static_cast<int64_t>(s.qn) * p.group <= p.few_rows ? kv4_units(s.len) : 0;
+  };
   auto weight = [&](const Kv4Seq &s) -> int64_t {
     return static_cast<int64_t>(units_of(s)) * p.geom.heads;
   };
@@ -164,6 +182,396 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
         } while (units == 0);
       }
     }
+  }
+}
+
+// ------------------------------------------------------------------ many rows
+
+namespace kv4_wprompt_cfg {
+constexpr int kThreads = 448;
+constexpr int kLoadWarp = 8;         // .. 11: queries, keys
+constexpr int kMmaWarp = 12;
+constexpr int kItemWarp = 13;
+constexpr int kTok = 128;            // tokens of an item
+constexpr int kRows = 128;           // query rows of a tile, at most
+constexpr int kStages = 4;           // query tiles in shared memory
+constexpr int kLseStages = 16;       // their log-sum-exps
+constexpr int kBufs = 3;             // of the product, in TMEM
+constexpr int kItems = 4;
+constexpr int kItemReaders = 8 + 4 + 1;
+constexpr uint32_t kTile = kRows * 256, kHalf = kTile / 2;
+constexpr uint32_t kQOff = 1024;
+constexpr uint32_t kLseOff = kQOff + kStages * kTile;
+constexpr uint32_t kKsOff = kLseOff + kLseStages * kRows * 4;   // [2][128] key scales
+constexpr uint32_t kSumOff = kKsOff + 2 * kTok * 4;             // [2][128] sums of half the tiles
+constexpr uint32_t kSmemBytes = kSumOff + 2 * kTok * 4 + 1024;  // + alignment slack
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemK = 0, kTmemS = 128;   // 2 x 64 columns of keys, 3 x 128 of products
+constexpr uint32_t kIdesc = idesc_f16(128, 128);
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+}  // namespace kv4_wprompt_cfg
+
+// Tiles of kTok tokens in the order sequence, tile (the first, which most rows
+// see, first), head; taken in turns as the prompt attention's items are.
+struct Kv4WItem {
+  int b, head, tok0, more;
+  int q0, qn, len, row0;   // row0: first row of the first tile of rows
+  int tiles;               // of rows
+};
+
+__device__ __forceinline__ int64_t kv4_wprompt_weight(const Kv4Seq &s, const Kv4Weights &p) {
+  if (static_cast<int64_t>(s.qn) * p.group <= p.few_rows) return 0;
+  return static_cast<int64_t>((s.len + kv4_wprompt_cfg::kTok - 1) / kv4_wprompt_cfg::kTok) *
+         p.geom.heads;
+}
+
+__device__ __forceinline__ Kv4WItem kv4_wprompt_item(const Kv4Weights &p, int &b, int64_t &rest) {
+  using namespace kv4_wprompt_cfg;
+  Kv4Seq s;
+  for (;;) {
+    s = kv4_load_seq(p.seqs, b);
+    const int64_t w = kv4_wprompt_weight(s, p);
+    if (rest < w) break;
+    rest -= w;
+    ++b;
+  }
+  Kv4WItem it;
+  it.b = b;
+  const int at = static_cast<int>(rest / p.geom.heads);
+  it.head = static_cast<int>(rest - static_cast<int64_t>(at) * p.geom.heads);
+  it.tok0 = at * kTok;
+  it.q0 = s.q0;
+  it.qn = s.qn;
+  it.len = s.len;
+  // the first query that sees the first token
+  int qi = p.causal ? it.tok0 - (s.len - s.qn) : 0;
+  if (qi < 0) qi = 0;
+  it.row0 = qi * p.group / p.tile_rows * p.tile_rows;
+  it.tiles = (s.qn * p.group - it.row0 + p.tile_rows - 1) / p.tile_rows;
+  it.more = 1;
+  return it;
+}
+
+__global__ void __launch_bounds__(kv4_wprompt_cfg::kThreads, 1)
+kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
+                          const __grid_constant__ Kv4Weights p) {
+  using namespace kv4_wprompt_cfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem);   // [kStages] query tile stored
+  uint64_t *q_empty = q_full + kStages;     // [kStages] its product complete
+  uint64_t *s_full = q_empty + kStages;     // [kBufs] product complete
+  uint64_t *s_empty = s_full + kBufs;       // [kBufs] product read
+  uint64_t *k_full = s_empty + kBufs;       // [2] keys in TMEM
+  uint64_t *k_empty = k_full + 2;           // [2] last product with them complete, scales read
+  uint64_t *sum_full = k_empty + 2;         // [2] second warpgroup's sums stored
+  uint64_t *sum_empty = sum_full + 2;       // [2] and read
+  uint64_t *item_full = sum_empty + 2;      // [kItems]
+  uint64_t *item_empty = item_full + kItems;
+  uint64_t *done = item_empty + kItems;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  Kv4WItem *ring = reinterpret_cast<Kv4WItem *>(tmem_slot + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&q_full[i], 4);      // one arrival per warp, here and below (+ the copies' bytes)
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 4);
+      mbar_init(&k_empty[i], 1 + 8);   // the last product, and the scales read
+      mbar_init(&sum_full[i], 4);
+      mbar_init(&sum_empty[i], 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kItemReaders);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  // rows of the query tiles that no copy reaches
+  for (uint32_t i = threadIdx.x; i < kStages * kTile / 16; i += kThreads)
+    st_shared_v4(smem + kQOff + 16 * i, 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  grid_dependency_wait();
+  const Kv4Line line = kv4_find_place<kThreads / 32>(
+      p.seqs, [&](const Kv4Seq &s) { return kv4_wprompt_weight(s, p); },
+      [](int64_t total) -> int64_t {
+        return blockIdx.x < total ? static_cast<int64_t>(blockIdx.x) : -1;
+      });
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tbase = *tmem_slot;
+  auto fail = [&]() {
+    report_status(6 /* ATOM_ERR_TIMEOUT */);
+    *abort_flag = 1;
+  };
+  uint32_t item_no = 0;
+  auto take_item = [&](Kv4WItem &it) -> bool {
+    const int slot = item_no % kItems;
+    const bool ok = mbar_wait_idle(&item_full[slot], (item_no / kItems) & 1, abort_flag, 64);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    it = ring[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[slot]);
+    ++item_no;
+    return true;
+  };
+  bool ok = true;
+
+  if (warp < 8) {
+    // ================================================================ sums
+    const int w = warp >> 2;                 // takes every second tile of rows
+    const int tid = threadIdx.x & 127;       // token of the item, TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    uint32_t tiles = 0, items = 0;           // so far, over all items
+    for (;;) {
+      Kv4WItem it;
+      if (!(ok = take_item(it)) || !it.more) break;
+      const int pos = it.tok0 + tid;
+      const bool valid = pos < it.len;
+      // first row that sees the token
+      const int sees = p.causal ? (pos - (it.len - it.qn)) * p.group : 0;
+      ok = mbar_wait_idle(&k_full[items & 1], (items >> 1) & 1, abort_flag, 32);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const float k = reinterpret_cast<const float *>(smem + kKsOff)[(items & 1) * kTok + tid];
+      const float2 k2 = make_float2(k, k);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_empty[items & 1]);
+      float sum = 0.f;
+      for (int i = (w - tiles) & 1; i < it.tiles; i += 2) {
+        const uint32_t no = tiles + i, buf = no % kBufs;
+        ok = mbar_wait_inline(&s_full[buf], (no / kBufs) & 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after_sync();
+        const uint32_t s_addr = tbase + lane_base + kTmemS + kRows * buf;
+        const float4 *lse = reinterpret_cast<const float4 *>(smem + kLseOff) +
+                            (no % kLseStages) * (kRows / 4);
+        const int from = sees - (it.row0 + i * p.tile_rows);   // first column that counts
+        const bool mask = __any_sync(0xffffffffu, from > 0);
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t raw[2][32];
+        tmem_ld_x32(s_addr, raw[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {   // the next columns are on their way meanwhile
+          tmem_ld_wait(raw[c & 1]);
+          if (c < 3) {
+            tmem_ld_x32(s_addr + 32 * (c + 1), raw[(c + 1) & 1]);
+          } else {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[buf]);
+          }
+          const uint32_t (&r)[32] = raw[c & 1];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 z = lse[8 * c + j];   // negative
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2 y = f2_fma(make_float2(__uint_as_float(r[4 * j + 2 * h]),
+                                            __uint_as_float(r[4 * j + 2 * h + 1])),
+                                k2, h == 0 ? make_float2(z.x, z.y) : make_float2(z.z, z.w));
+              y.x = exp2_approx(y.x);
+              y.y = exp2_approx(y.y);
+              if (mask) {
+                if (32 * c + 4 * j + 2 * h < from) y.x = 0.f;
+                if (32 * c + 4 * j + 2 * h + 1 < from) y.y = 0.f;
+              }
+              part[h] = f2_add(part[h], y);
+            }
+          }
+        }
+        const float2 both = f2_add(part[0], part[1]);
+        sum += both.x + both.y;
+      }
+      if (!ok) break;
+      // ---- the two warpgroups' sums
+      float *other = reinterpret_cast<float *>(smem + kSumOff) + (items & 1) * kTok + tid;
+      if (w == 1) {
+        ok = mbar_wait_idle(&sum_empty[items & 1], ((items >> 1) & 1) ^ 1u, abort_flag, 32);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        *other = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sum_full[items & 1]);
+      } else {
+        ok = mbar_wait_idle(&sum_full[items & 1], (items >> 1) & 1, abort_flag, 32);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        sum += *other;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sum_empty[items & 1]);
+        if (valid) {
+          const int64_t at = (static_cast<int64_t>(it.b) * p.geom.heads + it.head) * p.width + pos;
+          p.sums[at] = p.prev != nullptr ? p.prev[at] + sum : sum;
+        }
+      }
+      tiles += it.tiles;
+      ++items;
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp < kMmaWarp) {
+    // ================================================================ load
+    const int lt = threadIdx.x - 32 * kLoadWarp;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    uint32_t tiles = 0, items = 0;
+    for (;;) {
+      Kv4WItem it;
+      if (!(ok = take_item(it)) || !it.more) break;
+      // ---- keys: a thread expands a token's vector into its TMEM lane
+      {
+        const int pos = it.tok0 + lt;
+        uint4 q[4] = {};
+        float k = 0.f;
+        if (pos < it.len) {
+          const int page_no = kv4_div(pos, p.geom.by_page);
+          const int page = __ldg(p.seqs.table + it.b * p.seqs.table_stride + page_no);
+          const int64_t vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, it.head);
+          if (vec < 0) {
+            report_status(1 /* ATOM_ERR_INVALID_ARG */);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              q[i] = __ldg(reinterpret_cast<const uint4 *>(p.k4 + vec * 64) + i);
+            k = __ldg(p.ks + vec) * p.scale_log2;
+          }
+        }
+        ok = mbar_wait_idle(&k_empty[items & 1], ((items >> 1) & 1) ^ 1u, abort_flag, 32);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after_sync();
+        const uint32_t k_addr = tbase + lane_base + kTmemK + 64 * (items & 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          uint32_t o[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 c = codes_f16_chunk(words[j], true);
+            o[4 * j] = c.x;
+            o[4 * j + 1] = c.y;
+            o[4 * j + 2] = c.z;
+            o[4 * j + 3] = c.w;
+          }
+          tmem_st_x16(k_addr + 16 * i, o);
+        }
+        reinterpret_cast<float *>(smem + kKsOff)[(items & 1) * kTok + lt] = k;
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[items & 1]);
+      }
+      // ---- query tiles, and this thread's row's log-sum-exp
+      const int rows = it.qn * p.group;
+      auto row_lse = [&](int i) -> float {
+        const int r = it.row0 + i * p.tile_rows + lt;
+        if (i >= it.tiles || lt >= p.tile_rows || r >= rows) return INFINITY;
+        const int qi = kv4_div(r, p.by_group);
+        const float z = __ldg(p.lse + static_cast<int64_t>(it.q0 + qi) * p.q_heads +
+                              it.head * p.group + r - qi * p.group);
+        return z == -INFINITY ? INFINITY : z * 1.44269504088896341f;   // one that saw nothing
+      };
+      float next = row_lse(0);
+      for (int i = 0; i < it.tiles; ++i, ++tiles) {
+        const uint32_t st = tiles % kStages;
+        const float z = next;
+        next = row_lse(i + 1);
+        ok = mbar_wait_idle(&q_empty[st], ((tiles / kStages) & 1) ^ 1u, abort_flag, 20);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        // (the stage was last read for the tile 16 before, t: the product that freed
+        // this tile's stage, of tile t + 12, waited until product t + 9 was read, so
+        // the warps that take t's turn are past it)
+        reinterpret_cast<float *>(smem + kLseOff)[(tiles % kLseStages) * kRows + lt] = -z;
+        __syncwarp();
+        if (lt == 0) {
+          mbar_arrive_expect_tx(&q_full[st], p.tile_rows * 256);
+          const int tok = it.q0 + kv4_div(it.row0 + i * p.tile_rows, p.by_group);
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(smem + kQOff + st * kTile + h * kHalf, &q_map, 64 * h, it.head * p.group,
+                        tok, &q_full[st]);
+        } else if (lane == 0) {
+          mbar_arrive(&q_full[st]);
+        }
+      }
+      if (!ok) break;
+      ++items;
+    }
+    // copies in flight land before shared memory is released
+    if (!ok && lt == 0)
+      for (uint32_t no = tiles > kStages ? tiles - kStages : 0; no < tiles; ++no)
+        (void)mbar_wait(&q_full[no % kStages], (no / kStages) & 1, nullptr);
+    if (!ok && lane == 0) fail();
+  } else if (warp == kMmaWarp) {
+    // ================================================================ MMA issuer
+    uint32_t tiles = 0, items = 0;
+    const uint32_t q_lo = desc_lo_k(smem_addr(smem + kQOff));
+    const bool leader = elect_one();
+    for (;;) {
+      Kv4WItem it;
+      if (!(ok = take_item(it)) || !it.more) break;
+      ok = mbar_wait(&k_full[items & 1], (items >> 1) & 1, abort_flag);
+      for (int i = 0; ok && i < it.tiles; ++i, ++tiles) {
+        const uint32_t st = tiles % kStages, buf = tiles % kBufs;
+        ok = mbar_wait(&s_empty[buf], ((tiles / kBufs) & 1) ^ 1u, abort_flag) &&
+             mbar_wait(&q_full[st], (tiles / kStages) & 1, abort_flag);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after_sync();
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_ts(tbase + kTmemS + kRows * buf, tbase + kTmemK + 64 * (items & 1) + 8 * k,
+                       q_lo + ((st * kTile + (k >> 2) * kHalf + (k & 3) * 32) >> 4), kIdesc,
+                       k > 0 ? 1u : 0u);
+          tc_commit(&s_full[buf]);
+          tc_commit(&q_empty[st]);
+          if (i + 1 == it.tiles) tc_commit(&k_empty[items & 1]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      ++items;
+    }
+    if (!ok && lane == 0) fail();
+    // nothing may still write TMEM or read shared memory when they are released
+    if (leader) tc_commit(done);
+    (void)mbar_wait(done, 0, nullptr);
+  } else if (threadIdx.x == 32 * kItemWarp) {
+    // ================================================================ items
+    int b = line.b, turn = 0;
+    int64_t place = blockIdx.x, rest = line.rest;
+    for (uint32_t made = 0;; ++made) {
+      const int slot = made % kItems;
+      if (!(ok = mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64))) break;
+      Kv4WItem it{};
+      if (place < line.total) {
+        it = kv4_wprompt_item(p, b, rest);
+        const int grid = static_cast<int>(gridDim.x), i = static_cast<int>(blockIdx.x);
+        const int step = ++turn & 1 ? 2 * (grid - 1 - i) + 1 : 2 * i + 1;
+        place += step;
+        rest += step;
+      }
+      ring[slot] = it;
+      mbar_arrive(&item_full[slot]);
+      if (!it.more) break;
+    }
+    if (!ok) fail();
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tbase, kTmemCols);
   }
 }
 
