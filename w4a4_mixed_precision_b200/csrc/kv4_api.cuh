@@ -260,6 +260,7 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   p.q_heads = static_cast<int>(q_heads);
   p.group = static_cast<int>(q_heads / cache->heads);
   p.by_group = atomk::kv4_div_by(p.group);
+  p.magic = atomk::kKv4Magic;
   p.scale_log2 = scale * kLog2e;
   p.causal = causal != 0 ? 1 : 0;
   p.max_q = static_cast<int>(batch->max_q < rows ? batch->max_q : rows);
@@ -330,6 +331,7 @@ atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t
   p.scale_log2 = scale * kLog2e;
   p.causal = causal != 0 ? 1 : 0;
   p.by_group = atomk::kv4_div_by(p.group);
+  p.magic = atomk::kKv4Magic;
   p.prev = prev;
   p.sums = sums;
   p.width = width;

@@ -8,9 +8,17 @@
 // kc, vc are the signed 4-bit codes and ks, vs the vectors' scales. A scale
 // belongs to a token, which is a row of the products below, so it multiplies a
 // score or a weight instead of 128 elements, and the matrix instructions see
-// the codes themselves, which fp16 and bf16 hold exactly. The weights p * vs go
-// into the second product as the sum of two bf16 numbers: 16 bits of mantissa
-// with fp32's range, because vs spans whatever range the values had.
+// the codes themselves, which fp16 holds exactly.
+//
+// The weights p * vs go into the second product as fp16 (2^-11 relative, as wide
+// as the output's own rounding; nothing else is rounded to 16 bits). vs spans
+// what the values spanned, so the scales of each 32 tokens are divided by 2^e, e
+// the exponent of their maximum, and a row's reference R is the running maximum
+// of (its largest x among them) + e, x = s log2(e): the weight 2^(x + e - R + 4)
+// vs 2^-e is then at most 2^15 (R lags by up to 11 before the sums are rescaled)
+// whatever the scales are. It keeps fp16's full precision down to 2^-18 of R's
+// own, and an absolute error of 2^-29 of the tokens' largest value below. The
+// sum of weights uses the same reference.
 //
 // What bounds it: 136 bytes per cached token and KV head (64 + 4 each of keys
 // and values) against 4 * 128 * rows operations, far below the tensor cores'
@@ -35,12 +43,22 @@
 // second kernel joins each tile's shares.
 #pragma once
 
-#include <cuda_bf16.h>
-
 #include "kv4_plan.h"
 #include "ptx.cuh"
 
 namespace atomk {
+
+// A nibble n is the code (n ^ 8) - 8. fp16 pairs of nibbles 0 and 4 of w: the
+// bits 0x6400 | (n ^ 8) are 1024 + (n ^ 8), exactly, and 1032 is subtracted; of
+// nibbles 1 and 5: 0x6400 | 16 (n ^ 8) is 1024 + 16 (n ^ 8), and / 16 - 72 is
+// exact. One LOP3 masks and sets the upper bits, if the latter come from a
+// register: it takes one immediate. The compiler, which knows constants, makes
+// two of it (142 instead of 64 LOP3 per 16 tokens of the decode kernel, on the
+// pipe that bounded it), so the two words come with the kernel's arguments.
+struct Kv4Magic {
+  uint32_t lo, hi;   // 0x64086408, 0x64806480
+};
+constexpr Kv4Magic kKv4Magic{0x64086408u, 0x64806480u};
 
 struct Kv4Attn {
   const __half *q;
@@ -61,10 +79,23 @@ struct Kv4Attn {
                                 // kernel, the others to the prompt kernel
   int split;                    // tiles may be shared between CTAs
   float *ws;                    // the shares (kv4_decode_cfg)
+  Kv4Magic magic;
 };
 
-// Log2-domain running maximum of a row that has seen nothing.
+// Reference of a row that has seen nothing.
 constexpr float kKv4NoMax = -1e30f;
+// Weights are raised by 2^kKv4Raise over the reference, which may lag by
+// 2^kKv4Lag behind the largest.
+constexpr float kKv4Raise = 4.f, kKv4Lag = 11.f;
+
+// Exponent e of a positive number's (its bits): the number < 2^e; and 2^-e.
+__device__ __forceinline__ int kv4_exponent(uint32_t bits) {
+  const int e = static_cast<int>(bits >> 23) - 126;
+  return e < -60 ? -60 : (e > 100 ? 100 : e);
+}
+__device__ __forceinline__ float kv4_down(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
 
 namespace kv4_decode_cfg {
 constexpr int kThreads = 128;
@@ -119,58 +150,33 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Transpose of an 8 x 8 matrix of 16-bit elements held as mma fragments.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// A nibble n is the code (n ^ 8) - 8. fp16 pairs of nibbles 0 and 4 of w: the
-// bits 0x6400 | (n ^ 8) are 1024 + (n ^ 8), exactly, and 1032 is subtracted.
-__device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w) {
-  const uint32_t m = (w & 0x000F000Fu) ^ 0x64086408u;
+__device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w, const Kv4Magic &c) {
+  const uint32_t m = (w & 0x000F000Fu) ^ c.lo;
   const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&m),
                             __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
-// Nibbles 1 and 5: 0x6400 | 16 (n ^ 8) is 1024 + 16 (n ^ 8); / 16 - 72 is exact.
-__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w) {
-  const uint32_t m = (w & 0x00F000F0u) ^ 0x64806480u;
+__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w, const Kv4Magic &c) {
+  const uint32_t m = (w & 0x00F000F0u) ^ c.hi;
   const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&m),
                             __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00)),
                             __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480)));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
-// bf16 pair of nibbles 0 and 4: 0x4300 | (n ^ 8) is 128 + (n ^ 8).
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  const uint32_t m = (w & 0x000F000Fu) ^ 0x43084308u;
-  const __nv_bfloat162 c = __halves2bfloat162(__ushort_as_bfloat16(0x4308),
-                                              __ushort_as_bfloat16(0x4308));
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), c);
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
 
-// The four key fragments' worth of pairs of a word: nibbles (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ void codes_f16_word(uint32_t w, uint32_t (&o)[4]) {
+// The four pairs of a word: nibbles (0,4) (1,5) (2,6) (3,7).
+__device__ __forceinline__ void codes_f16_word(uint32_t w, const Kv4Magic &c, uint32_t (&o)[4]) {
   const uint32_t w8 = w >> 8;
-  o[0] = codes_f16_lo(w);
-  o[1] = codes_f16_hi(w);
-  o[2] = codes_f16_lo(w8);
-  o[3] = codes_f16_hi(w8);
+  o[0] = codes_f16_lo(w, c);
+  o[1] = codes_f16_hi(w, c);
+  o[2] = codes_f16_lo(w8, c);
+  o[3] = codes_f16_hi(w8, c);
 }
 
 // Query fragments (B operand) of 8 query rows for codes_f16_word's order: lane
@@ -328,7 +334,7 @@ __device__ __forceinline__ int kv4_tile_end(const Kv4Walk &w, const Kv4Attn &p) 
 // row's log-sum-exp. A row that saw nothing has sum 0: zeros and -infinity.
 __device__ __forceinline__ void kv4_write_row(const Kv4Attn &p, int64_t row, int d,
                                               const float (&acc)[8], float top, float sum) {
-  const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
+  const float inv = sum > 0.f ? __fdiv_rn(exp2_approx(-kKv4Raise), sum) : 0.f;
   *reinterpret_cast<uint4 *>(p.out + row * 128 + d) =
       make_uint4(pack_half2_rn(acc[0] * inv, acc[1] * inv), pack_half2_rn(acc[2] * inv, acc[3] * inv),
                  pack_half2_rn(acc[4] * inv, acc[5] * inv), pack_half2_rn(acc[6] * inv, acc[7] * inv));
@@ -491,8 +497,8 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t ca[4], cb[4];
-            codes_f16_word(wa[j], ca);
-            codes_f16_word(wb[j], cb);
+            codes_f16_word(wa[j], p.magic, ca);
+            codes_f16_word(wb[j], p.magic, cb);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint32_t a[4] = {ca[2 * k], cb[2 * k], ca[2 * k + 1], cb[2 * k + 1]};
@@ -520,8 +526,9 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
               for (int e = 0; e < 4; ++e)
                 if (tok0 + 16 * h + g + 8 * (e >> 1) >= limit[n][e & 1]) x[n][h][e] = -INFINITY;
         }
-        // running maxima over the warp's tokens; a maximum that rose by less
-        // than 2^8 is left in place (weights up to 256 lose nothing in fp32)
+        const int e = kv4_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(sc[kTok + lane])));
+        const float ef = static_cast<float>(e), down = kv4_down(e);
+        // the references of the columns
         float mx[NT][2];
         bool rise = false;
 #pragma unroll
@@ -532,8 +539,8 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            mx[n][c] = v;
-            rise |= v > m[n][c] + 8.f;
+            mx[n][c] = v + ef;
+            rise |= mx[n][c] > m[n][c] + kKv4Lag;
           }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -551,30 +558,31 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
               }
             }
         }
+        // weights in their references, in the units 2^(e + kKv4Raise)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float add[2] = {ef + kKv4Raise - m[n][0], ef + kKv4Raise - m[n][1]};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[n][h][i] = exp2_approx(x[n][h][i] + add[i & 1]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float step = (x[n][0][c] + x[n][0][c + 2]) + (x[n][1][c] + x[n][1][c + 2]);
+            l[n][c] = fmaf(step, exp2_approx(-ef - kKv4Raise), l[n][c]);
+          }
+        }
         const uint8_t *vt = st + kCodeBytes + (4 * (t >> 1) + (t & 1)) * 64 +
                             (((g >> 1) ^ (t & 2)) << 4) + ((g & 1) << 3);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float v0 = sc[kTok + 16 * h + g], v1 = sc[kTok + 16 * h + g + 8];
-          // weights times value scales, as B operands of two bf16 parts
-          uint32_t hi[NT][2], lo[NT][2];
+          const float v0 = sc[kTok + 16 * h + g] * down, v1 = sc[kTok + 16 * h + g + 8] * down;
+          // weights times value scales, as B operands
+          uint32_t wf[NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[e] = exp2_approx(x[n][h][e] - m[n][e & 1]);
-              l[n][e & 1] += w[e];
-              w[e] *= e < 2 ? v0 : v1;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t b = pack_bf16x2(w[2 * i], w[2 * i + 1]);
-              const float r0 = w[2 * i] - __uint_as_float(b << 16);
-              const float r1 = w[2 * i + 1] - __uint_as_float(b & 0xFFFF0000u);
-              hi[n][i] = movmatrix(b);
-              lo[n][i] = movmatrix(pack_bf16x2(r0, r1));
-            }
+            wf[n][0] = movmatrix(pack_half2_rn(x[n][h][0] * v0, x[n][h][1] * v0));
+            wf[n][1] = movmatrix(pack_half2_rn(x[n][h][2] * v1, x[n][h][3] * v1));
           }
           // values: two words (16 elements) of the tokens 2t, 2t+1, 2t+8, 2t+9
           uint2 v[4];
@@ -586,17 +594,14 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
             const bool up = (i & 1) != 0;
             const uint32_t a0 = i < 2 ? v[0].x : v[0].y, a1 = i < 2 ? v[1].x : v[1].y;
             const uint32_t a2 = i < 2 ? v[2].x : v[2].y, a3 = i < 2 ? v[3].x : v[3].y;
-            const uint32_t ab = __byte_perm(a0, a1, up ? 0x7632 : 0x5410);
-            const uint32_t cd = __byte_perm(a2, a3, up ? 0x7632 : 0x5410);
+            uint32_t ab[4], cd[4];   // elements 4i .. 4i + 3 of two tokens each
+            codes_f16_word(__byte_perm(a0, a1, up ? 0x7632 : 0x5410), p.magic, ab);
+            codes_f16_word(__byte_perm(a2, a3, up ? 0x7632 : 0x5410), p.magic, cd);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t a[4] = {codes_bf16(ab >> (8 * k)), codes_bf16(ab >> (8 * k + 4)),
-                                     codes_bf16(cd >> (8 * k)), codes_bf16(cd >> (8 * k + 4))};
+              const uint32_t a[4] = {ab[2 * k], ab[2 * k + 1], cd[2 * k], cd[2 * k + 1]};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma_bf16_16816(o[n][2 * i + k], a, hi[n][0], hi[n][1]);
-                mma_bf16_16816(o[n][2 * i + k], a, lo[n][0], lo[n][1]);
-              }
+              for (int n = 0; n < NT; ++n) mma_f16_16816(o[n][2 * i + k], a, wf[n][0], wf[n][1]);
             }
           }
         }

@@ -17,15 +17,10 @@
 // is W alone (2^-11 relative, as wide as the output's own rounding; an exact sum
 // of two halves would cost half as many matrix instructions again).
 //
-// The range of W. vs spans what the values spanned, so the scales of each 32
-// tokens are divided by 2^e, e the exponent of their maximum, and a row's
-// reference R is the running maximum of (its largest x among them) + e: W is
-// then at most 2^15 (R lags by up to 11 before the output is rescaled, W is
-// raised by 2^4) whatever the scales are, and W keeps fp16's full precision down
-// to 2^-18 of R's own, and an absolute error of 2^-29 of the tokens' largest
-// value below. The sum of weights uses the same reference. (One row of 32 that
-// outgrows R costs its warp the wait for the output so far: with a lag of 4 two
-// warps in five did so in every tile of the 4096-token prompt, with 8 one in ten.)
+// The references R and the exponents e of the value scales are kv4_attn.cuh's.
+// (One row of 32 that outgrows R costs its warp the wait for the output so far:
+// with a lag of 2^4 two warps in five did so in every tile of the 4096-token
+// prompt, with 2^8 one in ten, with 2^11 one in fifty.)
 //
 // Roles (640 threads, one CTA per SM, a persistent loop over the work):
 //   warps 0..3, 4..7     softmax of query tile 0 and 1: thread = row = TMEM lane
@@ -71,7 +66,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;       // + 128 * query tile; S + 64 * (tile & 1)
 constexpr uint32_t kIdescS = idesc_f16(128, kTok);
 constexpr uint32_t kIdescO = idesc_f16(128, 128) | (1u << 16);   // B is MN-major
-constexpr float kRaise = 4.f, kLag = 11.f;
+constexpr float kRaise = kKv4Raise, kLag = kKv4Lag;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 }  // namespace kv4_prompt_cfg
 
@@ -190,9 +185,9 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
 
 // A word of codes as a 16-byte chunk: in the order 0 4 1 5 2 6 3 7 that masking
 // gives, or in its own.
-__device__ __forceinline__ uint4 codes_f16_chunk(uint32_t w, bool in_order) {
+__device__ __forceinline__ uint4 codes_f16_chunk(uint32_t w, const Kv4Magic &magic, bool in_order) {
   uint32_t o[4];
-  codes_f16_word(w, o);
+  codes_f16_word(w, magic, o);
   if (!in_order) return make_uint4(o[0], o[1], o[2], o[3]);
   return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
                     __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
@@ -577,9 +572,8 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         float *sc = reinterpret_cast<float *>(smem + kScOff + (no % kScStages) * kScStage);
         if (value) {
           const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(scale));
-          int e = static_cast<int>(largest >> 23) - 126;   // every scale < 2^e
-          e = e < -60 ? -60 : (e > 100 ? 100 : e);
-          sc[kTok + 32 * ew + lane] = scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          const int e = kv4_exponent(largest);
+          sc[kTok + 32 * ew + lane] = scale * kv4_down(e);
           if (lane == 0) sc[2 * kTok + ew] = static_cast<float>(e);
         } else {
           sc[32 * ew + lane] = scale * p.scale_log2;
@@ -591,7 +585,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
           const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 c = codes_f16_chunk(words[k], !value);
+            const uint4 c = codes_f16_chunk(words[k], p.magic, !value);
             st_shared_v4(dst + (((4 * (t & 1) + k) ^ (row & 7)) << 4), c.x, c.y, c.z, c.w);
           }
         }

@@ -43,6 +43,7 @@ struct Kv4Weights {
   const float *prev;     // [batch][heads][width], or null
   float *sums;           // [batch][heads][width]
   int64_t width;
+  Kv4Magic magic;
 };
 
 constexpr int kKv4WeightThreads = 128;
@@ -97,8 +98,8 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t ca[4], cb[4];
-          codes_f16_word(wa[j], ca);
-          codes_f16_word(wb[j], cb);
+          codes_f16_word(wa[j], p.magic, ca);
+          codes_f16_word(wb[j], p.magic, cb);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             kf[h][2 * j + k][0] = ca[2 * k];
@@ -457,7 +458,7 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
           uint32_t o[16];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint4 c = codes_f16_chunk(words[j], true);
+            const uint4 c = codes_f16_chunk(words[j], p.magic, true);
             o[4 * j] = c.x;
             o[4 * j + 1] = c.y;
             o[4 * j + 2] = c.z;
