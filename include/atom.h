@@ -410,8 +410,8 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  * its 64 bytes of codes are at k4 + 64 v (v4 + 64 v), its scale is ks[v]
  * (vs[v]), both as atom_kv_quant writes them. A contiguous cache
  * [tokens][heads][128] quantized by atom_kv_quant is one page (page_stride any,
- * token_stride heads, head_stride 1). Any strides >= 0 are taken; writing to
- * vectors that coincide is the caller's error. k4, v4 16-byte aligned, ks, vs
+ * token_stride heads, head_stride 1). Any strides from 0 to 2^31 - 1 are taken;
+ * writing to vectors that coincide is the caller's error. k4, v4 16-byte aligned, ks, vs
  * 4-byte.
  *
  * atom_kv4_batch_t -- the sequences of a call, in device memory:

@@ -21,7 +21,7 @@ CHECKS = r"""
 using namespace atomk;
 extern "C" {
 int div_by(int n, int64_t d) { return kv4_div(n, kv4_div_by(d)); }
-int64_t vector_of(int page, int slot, int head, int pages, int64_t ps, int64_t ts, int64_t hs) {
+int64_t vector_of(int page, int slot, int head, int pages, int ps, int ts, int hs) {
   Kv4Geom g{};
   g.pages = pages; g.page_stride = ps; g.token_stride = ts; g.head_stride = hs;
   return kv4_vector(g, page, slot, head);
@@ -93,7 +93,7 @@ def plan(tmp_path_factory):
                     "-o", str(d / "plan.so")], check=True)
     lib = ct.CDLL(str(d / "plan.so"))
     lib.div_by.argtypes = [ct.c_int, ct.c_int64]
-    lib.vector_of.argtypes = [ct.c_int] * 4 + [ct.c_int64] * 3
+    lib.vector_of.argtypes = [ct.c_int] * 7
     lib.vector_of.restype = ct.c_int64
     lib.weight_key.argtypes, lib.weight_key.restype = [ct.c_uint32], ct.c_uint32
     lib.part_begin.argtypes, lib.part_begin.restype = [ct.c_int64, ct.c_int, ct.c_int], ct.c_int64
@@ -111,8 +111,8 @@ def test_division_by_the_page_size(plan):
 
 def test_vectors_and_bad_pages(plan):
     assert plan.vector_of(3, 5, 2, 4, 1000, 10, 1) == 3052
-    assert plan.vector_of(2 ** 31 - 2, 2 ** 31 - 1, 7, 2 ** 31 - 1, 2 ** 31, 8, 1) == (
-        (2 ** 31 - 2) * 2 ** 31 + (2 ** 31 - 1) * 8 + 7)          # far past 32 bits
+    top = 2 ** 31 - 1                                             # far past 32 bits
+    assert plan.vector_of(top - 1, top, 7, top, top, top, 1) == (top - 1) * top + top * top + 7
     for page in (-1, 4, 2 ** 31 - 1, -2 ** 31):
         assert plan.vector_of(page, 0, 0, 4, 1000, 10, 1) == -1
 
@@ -214,7 +214,8 @@ def both(lib, kw):
 @pytest.mark.parametrize("kw,expect", [
     (dict(c=dict(page_size=0)), SHAPE), (dict(c=dict(heads=0)), SHAPE),
     (dict(c=dict(pages=2 ** 31)), SHAPE), (dict(c=dict(page_size=2 ** 31)), SHAPE),
-    (dict(c=dict(token_stride=-1)), INVALID), (dict(c=dict(k4=0)), INVALID),
+    (dict(c=dict(token_stride=-1)), INVALID), (dict(c=dict(page_stride=2 ** 31)), SHAPE),
+    (dict(c=dict(k4=0)), INVALID),
     (dict(c=dict(vs=0)), INVALID), (dict(c=dict(v4=A16 + 8)), ALIGN),
     (dict(c=dict(ks=MIS)), ALIGN), (dict(b=dict(batch=-1)), INVALID),
     (dict(b=dict(batch=2 ** 31)), SHAPE), (dict(b=dict(table_stride=1)), SHAPE),

@@ -12,7 +12,8 @@ atom_status_t kv4_check_cache(const atom_kv4_cache_t *c, bool touched) {
       c->head_stride < 0)
     return ATOM_ERR_INVALID_ARG;
   if (c->page_size < 1 || c->heads < 1 || !kv4_fits(c->pages) || !kv4_fits(c->page_size) ||
-      !kv4_fits(c->heads))
+      !kv4_fits(c->heads) || !kv4_fits(c->page_stride) || !kv4_fits(c->token_stride) ||
+      !kv4_fits(c->head_stride))
     return ATOM_ERR_SHAPE;
   if (!touched) return ATOM_OK;
   if (!c->k4 || !c->ks || !c->v4 || !c->vs) return ATOM_ERR_INVALID_ARG;
@@ -49,9 +50,10 @@ atom_status_t kv4_check_rows(const void *x, int64_t token, int64_t head) {
 
 atomk::Kv4Geom kv4_geom(const atom_kv4_cache_t *c) {
   atomk::Kv4Geom g;
-  g.page_stride = c->page_stride;
-  g.token_stride = c->token_stride;
-  g.head_stride = c->head_stride;
+  // (a dimension of one has no stride)
+  g.page_stride = c->pages > 1 ? static_cast<int>(c->page_stride) : 0;
+  g.token_stride = c->page_size > 1 ? static_cast<int>(c->token_stride) : 0;
+  g.head_stride = c->heads > 1 ? static_cast<int>(c->head_stride) : 0;
   g.pages = static_cast<int>(c->pages);
   g.page_size = static_cast<int>(c->page_size);
   g.heads = static_cast<int>(c->heads);
@@ -263,6 +265,8 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   p.magic = atomk::kKv4Magic;
   p.scale_log2 = scale * kLog2e;
   p.causal = causal != 0 ? 1 : 0;
+  // (one address a stage instead of one a token: 64x8192 123 -> XXX us)
+  p.whole = cache->page_size % 32 == 0;
   p.max_q = static_cast<int>(batch->max_q < rows ? batch->max_q : rows);
   // Sequences with up to 16 query rows a KV head go to the decode kernel, those
   // with more to the prompt kernel; one that no sequence can need is not launched.

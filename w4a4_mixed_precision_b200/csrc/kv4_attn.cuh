@@ -78,6 +78,7 @@ struct Kv4Attn {
   int few_rows;                 // sequences of up to so many rows a KV head go to the decode
                                 // kernel, the others to the prompt kernel
   int split;                    // tiles may be shared between CTAs
+  int whole;                    // 32 tokens that begin at a multiple of 32 share a page
   float *ws;                    // the shares (kv4_decode_cfg)
   Kv4Magic magic;
 };
@@ -389,39 +390,75 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
   int l_end = kv4_tile_end<NT>(lw, p);
   uint8_t *ring = kv4_smem + warp * kRing;
   const uint32_t ring_addr = smem_addr(ring);
-  int page_no, page;   // of the next stage's token `lane` of this warp
+  // Lane (g, t) copies chunk t of the tokens g, g + 8, ... Token i of 16 (bits
+  // k t1 t0 j) of the values goes to row (k t1 j t0), chunks exchanged by t1: the
+  // 8-byte loads below then meet no bank twice.
+  const uint32_t k_dst = ring_addr + lane * 16;
+  const uint32_t v_dst = ring_addr + kCodeBytes +
+                         (((g & ~3) | ((g & 1) << 1) | ((g >> 1) & 1)) << 6) + ((t ^ ((g >> 1) & 2)) << 4);
+  const uint32_t s_dst = ring_addr + 2 * kCodeBytes + lane * 4;
+  const int64_t lane_scale = static_cast<int64_t>(lane) * p.geom.token_stride;
+  const int64_t lane_code = static_cast<int64_t>(g) * p.geom.token_stride * 64 + t * 16;
+  const int64_t step = static_cast<int64_t>(p.geom.token_stride) * 512;
+  int page_no, page;   // of the next stage's first token, or (not whole) of token `lane`
   auto fetch_page = [&]() {
-    const int pos = lw.unit * kKv4Unit + warp * kTok + lane;
+    const int pos = lw.unit * kKv4Unit + warp * kTok + (p.whole ? 0 : lane);
     page_no = kv4_div(pos, p.geom.by_page);
     page = pos < l_end ? __ldg(p.seqs.table + lw.b * p.seqs.table_stride + page_no) : -1;
   };
   fetch_page();
   auto issue = [&](int stage) {
     if (to_load > 0) {
-      const int pos = lw.unit * kKv4Unit + warp * kTok + lane;
-      if (pos - lane < l_end) {   // else: nothing of this warp's share is seen
+      const int pos0 = lw.unit * kKv4Unit + warp * kTok;
+      const uint32_t at = stage * kStage;
+      if (pos0 >= l_end) {
+        // nothing of this warp's share is seen
+      } else if (p.whole) {
+        // the stage's tokens are in one page
+        int n = l_end - pos0;
+        int64_t vec = kv4_vector(p.geom, page, pos0 - page_no * p.geom.page_size, lw.head);
+        if (vec < 0) {
+          report_status(1 /* ATOM_ERR_INVALID_ARG */);
+          vec = 0;
+          n = 0;
+        }
+        const int64_t scale = vec + (lane < n ? lane_scale : 0);
+        cp_async_4z(s_dst + at, p.ks + scale, lane < n ? 4u : 0u);
+        cp_async_4z(s_dst + at + kTok * 4, p.vs + scale, lane < n ? 4u : 0u);
+        const uint8_t *kp = p.k4 + lane_code + vec * 64, *vp = p.v4 + lane_code + vec * 64;
+        if (n >= kTok) {
+#pragma unroll
+          for (int i = 0; i < kTok / 8; ++i) {
+            cp_async_16(k_dst + at + i * 512, kp, 16u);
+            cp_async_16(v_dst + at + i * 512, vp, 16u);
+            kp += step;
+            vp += step;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTok / 8; ++i) {
+            const bool is = 8 * i + g < n;
+            cp_async_16(k_dst + at + i * 512, is ? kp + i * step : p.k4, is ? 16u : 0u);
+            cp_async_16(v_dst + at + i * 512, is ? vp + i * step : p.v4, is ? 16u : 0u);
+          }
+        }
+      } else {
+        const int pos = pos0 + lane;
         int64_t vec = -1;
         if (pos < l_end) {
           vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, lw.head);
           if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
         }
-        const uint32_t base = ring_addr + stage * kStage;
-        const uint32_t sc = base + 2 * kCodeBytes + lane * 4;
         const int64_t safe = vec < 0 ? 0 : vec;
-        cp_async_4z(sc, p.ks + safe, vec < 0 ? 0u : 4u);
-        cp_async_4z(sc + kTok * 4, p.vs + safe, vec < 0 ? 0u : 4u);
+        cp_async_4z(s_dst + at, p.ks + safe, vec < 0 ? 0u : 4u);
+        cp_async_4z(s_dst + at + kTok * 4, p.vs + safe, vec < 0 ? 0u : 4u);
 #pragma unroll
         for (int i = 0; i < kTok / 8; ++i) {
-          const int tok = 8 * i + g;   // this lane copies chunk t of token tok
-          const int64_t v = __shfl_sync(0xffffffffu, vec, tok);
+          const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
           const int64_t off = (v < 0 ? 0 : v) * 64 + t * 16;
           const uint32_t bytes = v < 0 ? 0u : 16u;
-          cp_async_16(base + tok * 64 + t * 16, p.k4 + off, bytes);
-          // values: token i of 16 (bits k t1 t0 j) in row (k t1 j t0), chunks
-          // exchanged by t1: the 8-byte loads below then meet no bank twice
-          const int r = (tok & ~3) | ((tok & 1) << 1) | ((tok >> 1) & 1);
-          const int c = t ^ ((tok >> 1) & 2);
-          cp_async_16(base + kCodeBytes + r * 64 + c * 16, p.v4 + off, bytes);
+          cp_async_16(k_dst + at + i * 512, p.k4 + off, bytes);
+          cp_async_16(v_dst + at + i * 512, p.v4 + off, bytes);
         }
       }
       const bool last = lw.unit + 1 >= lw.units;

@@ -35,7 +35,7 @@ KV4_HD int kv4_div(int n, const Kv4Div &d) {
 // A cache's geometry. Vectors (one token of one head) are addressed by number:
 // vector v has its 64 bytes of codes at 64 v and its scale at v.
 struct Kv4Geom {
-  int64_t page_stride, token_stride, head_stride;   // in vectors
+  int page_stride, token_stride, head_stride;   // in vectors
   int pages, page_size, heads;
   Kv4Div by_page;
 };
@@ -67,7 +67,8 @@ KV4_HD Kv4Seq kv4_seq_of(int q0, int q1, int len, int rows, int capacity) {
 // Vector number of (page, slot, head), or -1 for a page outside the cache.
 KV4_HD int64_t kv4_vector(const Kv4Geom &c, int page, int slot, int head) {
   if (page < 0 || page >= c.pages) return -1;
-  return page * c.page_stride + slot * c.token_stride + head * c.head_stride;
+  return static_cast<int64_t>(page) * c.page_stride + static_cast<int64_t>(slot) * c.token_stride +
+         static_cast<int64_t>(head) * c.head_stride;
 }
 
 // Cached positions a query may see: all, or (causal) those up to its own.
