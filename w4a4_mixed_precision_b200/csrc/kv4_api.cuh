@@ -336,6 +336,7 @@ atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t
   p.causal = causal != 0 ? 1 : 0;
   p.by_group = atomk::kv4_div_by(p.group);
   p.magic = atomk::kKv4Magic;
+  p.whole = cache->page_size % 32 == 0;
   p.prev = prev;
   p.sums = sums;
   p.width = width;
@@ -361,8 +362,8 @@ atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t
                      q_map, p);
   }
   if (err == cudaSuccess && few)
-    err = kv4_launch(atomk::kv4_weights_kernel, 4 * dev->sm_count, atomk::kKv4WeightThreads, 0,
-                     stream, p);
+    err = kv4_launch(atomk::kv4_weights_kernel, 5 * dev->sm_count,
+                     atomk::kv4_wdecode_cfg::kThreads, 0, stream, p);
   return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 

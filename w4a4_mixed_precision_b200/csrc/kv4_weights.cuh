@@ -38,6 +38,7 @@ struct Kv4Weights {
   int tile_rows;         // query rows of a tile: whole tokens' rows, up to 128
   float scale_log2;
   int causal;
+  int whole;             // as in Kv4Attn
   int few_rows;          // sequences of up to so many rows a KV head go to the first
                          // kernel, the others to the second
   const float *prev;     // [batch][heads][width], or null
@@ -46,55 +47,166 @@ struct Kv4Weights {
   Kv4Magic magic;
 };
 
-constexpr int kKv4WeightThreads = 128;
+namespace kv4_wdecode_cfg {
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kTok = 32;             // tokens per warp and stage
+constexpr int kStages = 4;
+constexpr uint32_t kCodeBytes = kTok * 64;
+constexpr uint32_t kStage = kCodeBytes + kTok * 4;   // codes, scales
+constexpr uint32_t kSmemBytes = kWarps * kStages * kStage;
+}  // namespace kv4_wdecode_cfg
 
-__global__ void __launch_bounds__(kKv4WeightThreads, 4)
+// A unit of 128 tokens of a (sequence, KV head), with its sequence's facts.
+struct Kv4WUnit {
+  int b, head, unit, units;
+  Kv4Seq s;
+};
+
+__device__ __forceinline__ int kv4_wdecode_units(const Kv4Seq &s, const Kv4Weights &p) {
+  return s.len > 0 && static_cast<int64_t>(s.qn) * p.group <= p.few_rows ? kv4_units(s.len) : 0;
+}
+__device__ __forceinline__ void kv4_next_unit(Kv4WUnit &u, const Kv4Weights &p) {
+  if (++u.unit < u.units) return;
+  u.unit = 0;
+  if (++u.head < p.geom.heads) return;
+  u.head = 0;
+  do {
+    ++u.b;
+    u.s = kv4_load_seq(p.seqs, u.b);
+    u.units = kv4_wdecode_units(u.s, p);
+  } while (u.units == 0);
+}
+
+__global__ void __launch_bounds__(kv4_wdecode_cfg::kThreads, 5)
 kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
-  constexpr int kWarps = kKv4WeightThreads / 32;
+  using namespace kv4_wdecode_cfg;
+  __shared__ __align__(16) uint8_t ring_all[kSmemBytes];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   grid_dependency_wait();
-  auto units_of = [&](const Kv4Seq &s) {
-    return s.len > 0 && static_cast<int64_t>(s.qn) * p.group <= p.few_rows ? kv4_units(s.len) : 0;
-  };
-  auto weight = [&](const Kv4Seq &s) -> int64_t {
-    return static_cast<int64_t>(units_of(s)) * p.geom.heads;
-  };
-  const Kv4Part part = kv4_find_part<kWarps>(p.seqs, weight);
+  const Kv4Part part = kv4_find_part<kWarps>(p.seqs, [&](const Kv4Seq &s) -> int64_t {
+    return static_cast<int64_t>(kv4_wdecode_units(s, p)) * p.geom.heads;
+  });
   if (part.count == 0) return;
-  int b = part.b;
-  Kv4Seq s = kv4_load_seq(p.seqs, b);
-  int units = units_of(s);
-  int head = static_cast<int>(part.rest / units);
-  int unit = static_cast<int>(part.rest - static_cast<int64_t>(head) * units);
-  for (int64_t left = part.count; left > 0; --left) {
-    const int tok0 = unit * kKv4Unit + warp * 32;
-    if (tok0 < s.len) {
-      // ---- key fragments of 32 tokens: rows g, g + 8 of two halves
-      uint32_t kf[2][8][4];
-      float ks[2][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int pos = tok0 + 16 * h + 8 * i + g;
-          w[i] = make_uint4(0u, 0u, 0u, 0u);
-          ks[h][i] = 0.f;
-          if (pos < s.len) {
-            const int page_no = kv4_div(pos, p.geom.by_page);
-            const int page = __ldg(p.seqs.table + b * p.seqs.table_stride + page_no);
-            const int64_t vec =
-                kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, head);
-            if (vec < 0) {
-              report_status(1 /* ATOM_ERR_INVALID_ARG */);
-            } else {
-              w[i] = __ldg(reinterpret_cast<const uint4 *>(p.k4 + vec * 64 + t * 16));
-              ks[h][i] = __ldg(p.ks + vec) * p.scale_log2;
-            }
-          }
+  Kv4WUnit u;    // what is computed
+  u.b = part.b;
+  u.s = kv4_load_seq(p.seqs, u.b);
+  u.units = kv4_wdecode_units(u.s, p);
+  u.head = static_cast<int>(part.rest / u.units);
+  u.unit = static_cast<int>(part.rest - static_cast<int64_t>(u.head) * u.units);
+
+  // ---- the copies, kStages units ahead of the arithmetic (as kv4_attn.cuh's)
+  Kv4WUnit l = u;
+  int64_t to_load = part.count;
+  const uint8_t *ring = ring_all + warp * kStages * kStage;
+  const uint32_t k_dst = smem_addr(ring) + lane * 16, s_dst = smem_addr(ring) + kCodeBytes + lane * 4;
+  const int64_t lane_scale = static_cast<int64_t>(lane) * p.geom.token_stride;
+  const int64_t lane_code = static_cast<int64_t>(g) * p.geom.token_stride * 64 + t * 16;
+  const int64_t step = static_cast<int64_t>(p.geom.token_stride) * 512;
+  int page_no, page;   // of the next stage's first token, or (not whole) of token `lane`
+  auto fetch_page = [&]() {
+    const int pos = l.unit * kKv4Unit + warp * kTok + (p.whole ? 0 : lane);
+    page_no = kv4_div(pos, p.geom.by_page);
+    page = pos < l.s.len ? __ldg(p.seqs.table + l.b * p.seqs.table_stride + page_no) : -1;
+  };
+  fetch_page();
+  auto issue = [&](int stage) {
+    if (to_load > 0) {
+      const int pos0 = l.unit * kKv4Unit + warp * kTok;
+      const uint32_t at = stage * kStage;
+      if (pos0 >= l.s.len) {
+        // none of the sequence's tokens
+      } else if (p.whole) {
+        int n = l.s.len - pos0;
+        int64_t vec = kv4_vector(p.geom, page, pos0 - page_no * p.geom.page_size, l.head);
+        if (vec < 0) {
+          report_status(1 /* ATOM_ERR_INVALID_ARG */);
+          vec = 0;
+          n = 0;
         }
-        const uint32_t wa[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-        const uint32_t wb[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+        cp_async_4z(s_dst + at, p.ks + vec + (lane < n ? lane_scale : 0), lane < n ? 4u : 0u);
+        const uint8_t *kp = p.k4 + lane_code + vec * 64;
+#pragma unroll
+        for (int i = 0; i < kTok / 8; ++i) {
+          const bool is = 8 * i + g < n;
+          cp_async_16(k_dst + at + i * 512, is ? kp : p.k4, is ? 16u : 0u);
+          kp += step;
+        }
+      } else {
+        const int pos = pos0 + lane;
+        int64_t vec = -1;
+        if (pos < l.s.len) {
+          vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, l.head);
+          if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
+        }
+        cp_async_4z(s_dst + at, p.ks + (vec < 0 ? 0 : vec), vec < 0 ? 0u : 4u);
+#pragma unroll
+        for (int i = 0; i < kTok / 8; ++i) {
+          const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
+          cp_async_16(k_dst + at + i * 512, p.k4 + (v < 0 ? 0 : v) * 64 + t * 16, v < 0 ? 0u : 16u);
+        }
+      }
+      if (--to_load > 0) {
+        kv4_next_unit(l, p);
+        fetch_page();
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) issue(i);
+
+  // ---- query rows r0 .. r0 + 7 of the unit's (sequence, head): fragments, and
+  // the log-sum-exps and limits of this lane's two columns
+  uint32_t qf[16];
+  float lse[2];
+  int limit[2];
+  auto queries = [&](int r0, int rows) {
+    const int r = r0 + g;
+    const bool valid = r < rows;
+    const int qi = valid ? kv4_div(r, p.by_group) : 0;
+    const int hq = u.head * p.group + (valid ? r - qi * p.group : 0);
+    kv4_query_fragments(p.q + (u.s.q0 + qi) * p.q_token + hq * p.q_head, t, valid, qf);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int rc = r0 + 2 * t + c;
+      limit[c] = 0;
+      lse[c] = 0.f;
+      if (rc < rows) {
+        const int qc = kv4_div(rc, p.by_group);
+        limit[c] = kv4_limit(u.s, qc, p.causal != 0);
+        const float z = __ldg(p.lse + static_cast<int64_t>(u.s.q0 + qc) * p.q_heads +
+                              u.head * p.group + rc - qc * p.group);
+        lse[c] = z * 1.44269504088896341f;
+        if (z == -INFINITY) limit[c] = 0;   // a row that saw nothing
+      }
+    }
+  };
+
+  int had_b = -1, had_head = -1;   // whose rows the fragments hold, if it has one tile
+  int stage = 0;
+  for (int64_t left = part.count;;) {
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const int tok0 = u.unit * kKv4Unit + warp * kTok;
+    if (tok0 < u.s.len) {
+      const uint8_t *st = ring + stage * kStage;
+      const float *sc = reinterpret_cast<const float *>(st + kCodeBytes);
+      const int rows = u.s.qn * p.group;
+      // all query rows that see the first of the tokens, and those after
+      int qi0 = p.causal ? tok0 - (u.s.len - u.s.qn) : 0;
+      const int first = (qi0 < 0 ? 0 : qi0) * p.group / 8 * 8;
+      if (rows <= 8 && (u.b != had_b || u.head != had_head)) {
+        queries(0, rows);
+        had_b = u.b;
+        had_head = u.head;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {   // 16 tokens: rows g and g + 8 of the fragments
+        const uint4 ka = *reinterpret_cast<const uint4 *>(st + (16 * h + g) * 64 + t * 16);
+        const uint4 kb = *reinterpret_cast<const uint4 *>(st + (16 * h + g + 8) * 64 + t * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        uint32_t kf[8][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t ca[4], cb[4];
@@ -102,88 +214,58 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
           codes_f16_word(wb[j], p.magic, cb);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            kf[h][2 * j + k][0] = ca[2 * k];
-            kf[h][2 * j + k][1] = cb[2 * k];
-            kf[h][2 * j + k][2] = ca[2 * k + 1];
-            kf[h][2 * j + k][3] = cb[2 * k + 1];
+            kf[2 * j + k][0] = ca[2 * k];
+            kf[2 * j + k][1] = cb[2 * k];
+            kf[2 * j + k][2] = ca[2 * k + 1];
+            kf[2 * j + k][3] = cb[2 * k + 1];
           }
         }
-      }
-      // ---- all query rows that see the first of the tokens, and those after
-      const int rows = s.qn * p.group;
-      int qi0 = p.causal ? tok0 - (s.len - s.qn) : 0;
-      if (qi0 < 0) qi0 = 0;
-      float sum[2][2] = {}, far[2][2] = {};
-      int since = 0;
-      for (int r0 = qi0 * p.group / 8 * 8; r0 < rows; r0 += 8) {
-        uint32_t qf[16];
-        {
-          const int r = r0 + g;
-          const bool valid = r < rows;
-          const int qi = valid ? r / p.group : 0;
-          const int hq = head * p.group + (valid ? r - qi * p.group : 0);
-          kv4_query_fragments(p.q + (s.q0 + qi) * p.q_token + hq * p.q_head, t, valid, qf);
-        }
-        float lse[2];
-        int limit[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = r0 + 2 * t + c;
-          limit[c] = 0;
-          lse[c] = 0.f;
-          if (r < rows) {
-            const int qi = r / p.group, hq = head * p.group + r - qi * p.group;
-            limit[c] = kv4_limit(s, qi, p.causal != 0);
-            const float z = __ldg(p.lse + static_cast<int64_t>(s.q0 + qi) * p.q_heads + hq);
-            lse[c] = z * 1.44269504088896341f;
-            if (z == -INFINITY) limit[c] = 0;   // a row that saw nothing
+        const float s0 = sc[16 * h + g] * p.scale_log2, s1 = sc[16 * h + g + 8] * p.scale_log2;
+        const int pos = tok0 + 16 * h + g;
+        float sum[2] = {0.f, 0.f}, far[2] = {0.f, 0.f};
+        int since = 0;
+        for (int r0 = first; r0 < rows; r0 += 8) {
+          if (rows > 8) {
+            queries(r0, rows);
+            had_b = -1;
           }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
           float x[4] = {};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mma_f16_16816(x, kf[h][k], qf[2 * k], qf[2 * k + 1]);
+          for (int k = 0; k < 8; ++k) mma_f16_16816(x, kf[k], qf[2 * k], qf[2 * k + 1]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int pos = tok0 + 16 * h + 8 * (e >> 1) + g;
-            const float w = exp2_approx(fmaf(x[e], ks[h][e >> 1], -lse[e & 1]));
-            sum[h][e >> 1] += pos < limit[e & 1] ? w : 0.f;
+            const float w = exp2_approx(fmaf(x[e], e < 2 ? s0 : s1, -lse[e & 1]));
+            sum[e >> 1] += pos + 8 * (e >> 1) < limit[e & 1] ? w : 0.f;
+          }
+          if (++since == 32) {   // sums of sums: the rounding of long sums stays small
+            since = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              far[i] += sum[i];
+              sum[i] = 0.f;
+            }
           }
         }
-        if (++since == 32) {   // sums of sums: the rounding of long sums stays small
-          since = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            far[i >> 1][i & 1] += sum[i >> 1][i & 1];
-            sum[i >> 1][i & 1] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+          float v = far[i] + sum[i];
+          v += __shfl_xor_sync(0xffffffffu, v, 1);
+          v += __shfl_xor_sync(0xffffffffu, v, 2);
+          if (t == 0 && pos + 8 * i < u.s.len) {
+            const int64_t at =
+                (static_cast<int64_t>(u.b) * p.geom.heads + u.head) * p.width + pos + 8 * i;
+            p.sums[at] = p.prev != nullptr ? p.prev[at] + v : v;
           }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v = far[i >> 1][i & 1] + sum[i >> 1][i & 1];
-        v += __shfl_xor_sync(0xffffffffu, v, 1);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        const int pos = tok0 + 16 * (i >> 1) + 8 * (i & 1) + g;
-        if (t == 0 && pos < s.len) {
-          const int64_t at = (static_cast<int64_t>(b) * p.geom.heads + head) * p.width + pos;
-          p.sums[at] = p.prev != nullptr ? p.prev[at] + v : v;
         }
       }
     }
-    if (left > 1 && ++unit == units) {
-      unit = 0;
-      if (++head == p.geom.heads) {
-        head = 0;
-        do {
-          ++b;
-          s = kv4_load_seq(p.seqs, b);
-          units = units_of(s);
-        } while (units == 0);
-      }
-    }
+    if (--left == 0) break;
+    kv4_next_unit(u, p);
+    __syncwarp();
+    issue(stage);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ many rows
