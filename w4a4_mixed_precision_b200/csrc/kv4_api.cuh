@@ -336,7 +336,7 @@ atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t
   p.causal = causal != 0 ? 1 : 0;
   p.by_group = atomk::kv4_div_by(p.group);
   p.magic = atomk::kKv4Magic;
-  p.whole = cache->page_size % 32 == 0;
+  p.whole = cache->page_size % atomk::kv4_wdecode_cfg::kTok == 0;
   p.prev = prev;
   p.sums = sums;
   p.width = width;

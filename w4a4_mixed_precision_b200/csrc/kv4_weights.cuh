@@ -50,21 +50,23 @@ struct Kv4Weights {
 namespace kv4_wdecode_cfg {
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
-constexpr int kTok = 32;             // tokens per warp and stage
-constexpr int kStages = 4;
+constexpr int kTok = 64;             // tokens per warp and stage
+constexpr int kUnit = kWarps * kTok;
+constexpr int kStages = 2;
 constexpr uint32_t kCodeBytes = kTok * 64;
-constexpr uint32_t kStage = kCodeBytes + kTok * 4;   // codes, scales
+constexpr uint32_t kStage = kCodeBytes + 2 * kTok * 4;   // codes, scales, earlier sums
 constexpr uint32_t kSmemBytes = kWarps * kStages * kStage;
 }  // namespace kv4_wdecode_cfg
 
-// A unit of 128 tokens of a (sequence, KV head), with its sequence's facts.
+// A unit of 256 tokens of a (sequence, KV head), with its sequence's facts.
 struct Kv4WUnit {
   int b, head, unit, units;
   Kv4Seq s;
 };
 
 __device__ __forceinline__ int kv4_wdecode_units(const Kv4Seq &s, const Kv4Weights &p) {
-  return s.len > 0 && static_cast<int64_t>(s.qn) * p.group <= p.few_rows ? kv4_units(s.len) : 0;
+  return s.len > 0 && static_cast<int64_t>(s.qn) * p.group <= p.few_rows ? (s.len - 1) / kv4_wdecode_cfg::kUnit + 1
+                                                                             : 0;
 }
 __device__ __forceinline__ void kv4_next_unit(Kv4WUnit &u, const Kv4Weights &p) {
   if (++u.unit < u.units) return;
@@ -97,23 +99,31 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
 
   // ---- the copies, kStages units ahead of the arithmetic (as kv4_attn.cuh's)
   Kv4WUnit l = u;
-  int64_t to_load = part.count;
+  int to_load = static_cast<int>(part.count);
   const uint8_t *ring = ring_all + warp * kStages * kStage;
   const uint32_t k_dst = smem_addr(ring) + lane * 16, s_dst = smem_addr(ring) + kCodeBytes + lane * 4;
   const int64_t lane_scale = static_cast<int64_t>(lane) * p.geom.token_stride;
   const int64_t lane_code = static_cast<int64_t>(g) * p.geom.token_stride * 64 + t * 16;
   const int64_t step = static_cast<int64_t>(p.geom.token_stride) * 512;
-  int page_no, page;   // of the next stage's first token, or (not whole) of token `lane`
+  int page_no, page;   // of the next stage's first token (whole)
   auto fetch_page = [&]() {
-    const int pos = l.unit * kKv4Unit + warp * kTok + (p.whole ? 0 : lane);
+    const int pos = l.unit * kUnit + warp * kTok;
     page_no = kv4_div(pos, p.geom.by_page);
     page = pos < l.s.len ? __ldg(p.seqs.table + l.b * p.seqs.table_stride + page_no) : -1;
   };
-  fetch_page();
+  if (p.whole) fetch_page();
   auto issue = [&](int stage) {
     if (to_load > 0) {
-      const int pos0 = l.unit * kKv4Unit + warp * kTok;
+      const int pos0 = l.unit * kUnit + warp * kTok;
       const uint32_t at = stage * kStage;
+      if (pos0 < l.s.len && p.prev != nullptr) {
+        const float *src = p.prev + (static_cast<int64_t>(l.b) * p.geom.heads + l.head) * p.width + pos0;
+#pragma unroll
+        for (int i = 0; i < kTok; i += 32) {
+          const bool is = pos0 + i + lane < l.s.len;
+          cp_async_4z(s_dst + at + kTok * 4 + i * 4, is ? src + i + lane : p.prev, is ? 4u : 0u);
+        }
+      }
       if (pos0 >= l.s.len) {
         // none of the sequence's tokens
       } else if (p.whole) {
@@ -124,7 +134,13 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
           vec = 0;
           n = 0;
         }
-        cp_async_4z(s_dst + at, p.ks + vec + (lane < n ? lane_scale : 0), lane < n ? 4u : 0u);
+#pragma unroll
+        for (int i = 0; i < kTok; i += 32) {
+          const bool is = i + lane < n;
+          cp_async_4z(s_dst + at + i * 4,
+                      p.ks + vec + (is ? lane_scale + static_cast<int64_t>(i) * p.geom.token_stride : 0),
+                      is ? 4u : 0u);
+        }
         const uint8_t *kp = p.k4 + lane_code + vec * 64;
 #pragma unroll
         for (int i = 0; i < kTok / 8; ++i) {
@@ -133,22 +149,27 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
           kp += step;
         }
       } else {
-        const int pos = pos0 + lane;
-        int64_t vec = -1;
-        if (pos < l.s.len) {
-          vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, l.head);
-          if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
-        }
-        cp_async_4z(s_dst + at, p.ks + (vec < 0 ? 0 : vec), vec < 0 ? 0u : 4u);
+        for (int j = 0; j < kTok; j += 32) {
+          const int pos = pos0 + j + lane;
+          int64_t vec = -1;
+          if (pos < l.s.len) {
+            const int no = kv4_div(pos, p.geom.by_page);
+            vec = kv4_vector(p.geom, __ldg(p.seqs.table + l.b * p.seqs.table_stride + no),
+                             pos - no * p.geom.page_size, l.head);
+            if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
+          }
+          cp_async_4z(s_dst + at + j * 4, p.ks + (vec < 0 ? 0 : vec), vec < 0 ? 0u : 4u);
 #pragma unroll
-        for (int i = 0; i < kTok / 8; ++i) {
-          const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
-          cp_async_16(k_dst + at + i * 512, p.k4 + (v < 0 ? 0 : v) * 64 + t * 16, v < 0 ? 0u : 16u);
+          for (int i = 0; i < 4; ++i) {
+            const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
+            cp_async_16(k_dst + at + j * 64 + i * 512, p.k4 + (v < 0 ? 0 : v) * 64 + t * 16,
+                        v < 0 ? 0u : 16u);
+          }
         }
       }
       if (--to_load > 0) {
         kv4_next_unit(l, p);
-        fetch_page();
+        if (p.whole) fetch_page();
       }
     }
     cp_async_commit();
@@ -160,7 +181,7 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
   // the log-sum-exps and limits of this lane's two columns
   uint32_t qf[16];
   float lse[2];
-  int limit[2];
+  int limit[2], least = 0;   // least: of the warp's columns that count
   auto queries = [&](int r0, int rows) {
     const int r = r0 + g;
     const bool valid = r < rows;
@@ -170,93 +191,105 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int rc = r0 + 2 * t + c;
-      limit[c] = 0;
-      lse[c] = 0.f;
+      limit[c] = INT32_MAX;
+      lse[c] = INFINITY;   // of a column that counts for nothing
       if (rc < rows) {
         const int qc = kv4_div(rc, p.by_group);
-        limit[c] = kv4_limit(u.s, qc, p.causal != 0);
         const float z = __ldg(p.lse + static_cast<int64_t>(u.s.q0 + qc) * p.q_heads +
                               u.head * p.group + rc - qc * p.group);
-        lse[c] = z * 1.44269504088896341f;
-        if (z == -INFINITY) limit[c] = 0;   // a row that saw nothing
+        if (z != -INFINITY) {   // (a row that saw nothing)
+          limit[c] = kv4_limit(u.s, qc, p.causal != 0);
+          lse[c] = z * 1.44269504088896341f;
+        }
       }
     }
+    least = __reduce_min_sync(0xffffffffu, limit[0] < limit[1] ? limit[0] : limit[1]);
   };
 
   int had_b = -1, had_head = -1;   // whose rows the fragments hold, if it has one tile
   int stage = 0;
-  for (int64_t left = part.count;;) {
+  for (int left = static_cast<int>(part.count);;) {
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    const int tok0 = u.unit * kKv4Unit + warp * kTok;
+    const int tok0 = u.unit * kUnit + warp * kTok;
     if (tok0 < u.s.len) {
       const uint8_t *st = ring + stage * kStage;
       const float *sc = reinterpret_cast<const float *>(st + kCodeBytes);
       const int rows = u.s.qn * p.group;
       // all query rows that see the first of the tokens, and those after
-      int qi0 = p.causal ? tok0 - (u.s.len - u.s.qn) : 0;
+      const int qi0 = p.causal ? tok0 - (u.s.len - u.s.qn) : 0;
       const int first = (qi0 < 0 ? 0 : qi0) * p.group / 8 * 8;
       if (rows <= 8 && (u.b != had_b || u.head != had_head)) {
         queries(0, rows);
         had_b = u.b;
         had_head = u.head;
       }
+      float *to = p.sums + (static_cast<int64_t>(u.b) * p.geom.heads + u.head) * p.width + tok0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {   // 16 tokens: rows g and g + 8 of the fragments
-        const uint4 ka = *reinterpret_cast<const uint4 *>(st + (16 * h + g) * 64 + t * 16);
-        const uint4 kb = *reinterpret_cast<const uint4 *>(st + (16 * h + g + 8) * 64 + t * 16);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-        uint32_t kf[8][4];
+      for (int q = 0; q < kTok; q += 32) {
+        float v[4];   // sums of the tokens 8 i + g
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t ca[4], cb[4];
-          codes_f16_word(wa[j], p.magic, ca);
-          codes_f16_word(wb[j], p.magic, cb);
+        for (int h = 0; h < 2; ++h) {   // 16 tokens: rows g and g + 8 of the fragments
+          const int row = q + 16 * h + g;
+          const uint4 ka = *reinterpret_cast<const uint4 *>(st + row * 64 + t * 16);
+          const uint4 kb = *reinterpret_cast<const uint4 *>(st + (row + 8) * 64 + t * 16);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+          uint32_t kf[8][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            kf[2 * j + k][0] = ca[2 * k];
-            kf[2 * j + k][1] = cb[2 * k];
-            kf[2 * j + k][2] = ca[2 * k + 1];
-            kf[2 * j + k][3] = cb[2 * k + 1];
-          }
-        }
-        const float s0 = sc[16 * h + g] * p.scale_log2, s1 = sc[16 * h + g + 8] * p.scale_log2;
-        const int pos = tok0 + 16 * h + g;
-        float sum[2] = {0.f, 0.f}, far[2] = {0.f, 0.f};
-        int since = 0;
-        for (int r0 = first; r0 < rows; r0 += 8) {
-          if (rows > 8) {
-            queries(r0, rows);
-            had_b = -1;
-          }
-          float x[4] = {};
+          for (int j = 0; j < 4; ++j) {
+            uint32_t ca[4], cb[4];
+            codes_f16_word(wa[j], p.magic, ca);
+            codes_f16_word(wb[j], p.magic, cb);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mma_f16_16816(x, kf[k], qf[2 * k], qf[2 * k + 1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = exp2_approx(fmaf(x[e], e < 2 ? s0 : s1, -lse[e & 1]));
-            sum[e >> 1] += pos + 8 * (e >> 1) < limit[e & 1] ? w : 0.f;
-          }
-          if (++since == 32) {   // sums of sums: the rounding of long sums stays small
-            since = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              far[i] += sum[i];
-              sum[i] = 0.f;
+            for (int k = 0; k < 2; ++k) {
+              kf[2 * j + k][0] = ca[2 * k];
+              kf[2 * j + k][1] = cb[2 * k];
+              kf[2 * j + k][2] = ca[2 * k + 1];
+              kf[2 * j + k][3] = cb[2 * k + 1];
             }
           }
-        }
+          const float s0 = sc[row] * p.scale_log2, s1 = sc[row + 8] * p.scale_log2;
+          // (sums of sums: the rounding of long ones stays small)
+          float sum[2] = {0.f, 0.f}, far[2] = {0.f, 0.f};
+          for (int r0 = first; r0 < rows; r0 += 8) {
+            if (rows > 8) {
+              queries(r0, rows);
+              had_b = -1;
+            }
+            float x[4] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float v = far[i] + sum[i];
-          v += __shfl_xor_sync(0xffffffffu, v, 1);
-          v += __shfl_xor_sync(0xffffffffu, v, 2);
-          if (t == 0 && pos + 8 * i < u.s.len) {
-            const int64_t at =
-                (static_cast<int64_t>(u.b) * p.geom.heads + u.head) * p.width + pos + 8 * i;
-            p.sums[at] = p.prev != nullptr ? p.prev[at] + v : v;
+            for (int k = 0; k < 8; ++k) mma_f16_16816(x, kf[k], qf[2 * k], qf[2 * k + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = exp2_approx(fmaf(x[e], e < 2 ? s0 : s1, -lse[e & 1]));
+            if (tok0 + q + 32 > least) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (tok0 + row + 8 * (e >> 1) >= limit[e & 1]) x[e] = 0.f;
+            }
+            sum[0] += x[0] + x[1];
+            sum[1] += x[2] + x[3];
+            if (((r0 >> 3) & 31) == 31) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                far[i] += sum[i];
+                sum[i] = 0.f;
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float w = far[i] + sum[i];
+            w += __shfl_xor_sync(0xffffffffu, w, 1);
+            w += __shfl_xor_sync(0xffffffffu, w, 2);
+            v[2 * h + i] = w;
           }
         }
+        // lane (g, t) stores token 8 t + g
+        const int tok = q + 8 * t + g;
+        float w = t < 2 ? (t == 0 ? v[0] : v[1]) : (t == 2 ? v[2] : v[3]);
+        if (p.prev != nullptr) w += sc[kTok + tok];
+        if (tok0 + tok < u.s.len) to[tok] = w;
       }
     }
     if (--left == 0) break;
