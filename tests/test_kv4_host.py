@@ -45,7 +45,10 @@ int walk(const int *new_tokens, const int *lens, int batch, int heads, int group
   auto tiles = [&](int b) { return kv4_tiles(Kv4Seq{0, new_tokens[b], lens[b], true}, group, tile); };
   for (int b = 0; b < batch; ++b) total += int64_t(tiles(b)) * heads * kv4_units(lens[b]);
   *units_out = int(total);
-  const int parts = total < ctas ? int(total) : ctas;
+  int64_t rows = 0;
+  for (int b = 0; b < batch; ++b) rows += int64_t(tiles(b)) * heads;
+  const int parts = kv4_parts(total, rows, ctas);
+  if (total > 0 && (parts < 1 || parts > ctas || parts > total)) return 7;
   int64_t next = 0;
   // the tile of each place, as the line's order gives it
   struct Tile { int64_t begin, end; };

@@ -131,8 +131,8 @@ atom_status_t kv4_decode_ctas(DeviceState *dev, int nt, int *ctas) {
                                : reinterpret_cast<const void *>(atomk::kv4_decode_kernel<2>);
       int per_sm = 0;
       if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem_bytes(nt))) != cudaSuccess ||
-          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem_bytes(nt)) !=
+                               static_cast<int>(kSmemBytes)) != cudaSuccess ||
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, kSmemBytes) !=
               cudaSuccess ||
           per_sm < 1)
         return ATOM_ERR_CUDA;
@@ -265,8 +265,9 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   p.magic = atomk::kKv4Magic;
   p.scale_log2 = scale * kLog2e;
   p.causal = causal != 0 ? 1 : 0;
-  // (one address a stage instead of one a token: 64x8192 123 -> XXX us)
-  p.whole = cache->page_size % 32 == 0;
+  // One address a stage instead of one a token (64x8192: 103 us with pages of 64, 111
+  // with pages of 16).
+  p.whole = cache->page_size % atomk::kv4_decode_cfg::kTok == 0;
   p.max_q = static_cast<int>(batch->max_q < rows ? batch->max_q : rows);
   // Sequences with up to 16 query rows a KV head go to the decode kernel, those
   // with more to the prompt kernel; one that no sequence can need is not launched.
@@ -295,8 +296,8 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
     p.split = workspace != nullptr && aligned(workspace, 16) &&
               workspace_bytes >= static_cast<size_t>(ws_bytes(ctas, nt));
     p.ws = p.split ? static_cast<float *>(workspace) : nullptr;
-    err = nt == 1 ? kv4_launch(atomk::kv4_decode_kernel<1>, ctas, kThreads, smem_bytes(1), stream, p)
-                  : kv4_launch(atomk::kv4_decode_kernel<2>, ctas, kThreads, smem_bytes(2), stream, p);
+    err = nt == 1 ? kv4_launch(atomk::kv4_decode_kernel<1>, ctas, kThreads, kSmemBytes, stream, p)
+                  : kv4_launch(atomk::kv4_decode_kernel<2>, ctas, kThreads, kSmemBytes, stream, p);
     if (err == cudaSuccess && p.split)
       err = nt == 1
                 ? kv4_launch(atomk::kv4_join_kernel<1>, ctas, atomk::kKv4JoinThreads, 0, stream, p)

@@ -12,7 +12,7 @@
 //
 // The weights p * vs go into the second product as fp16 (2^-11 relative, as wide
 // as the output's own rounding; nothing else is rounded to 16 bits). vs spans
-// what the values spanned, so the scales of each 32 tokens are divided by 2^e, e
+// what the values spanned, so the scales of each 64 tokens are divided by 2^e, e
 // the exponent of their maximum, and a row's reference R is the running maximum
 // of (its largest x among them) + e, x = s log2(e): the weight 2^(x + e - R + 4)
 // vs 2^-e is then at most 2^15 (R lags by up to 11 before the sums are rescaled)
@@ -34,9 +34,9 @@
 // it; the second takes words of two tokens, exchanges their halves, and the
 // same masks give pairs of one element for the two tokens.
 //
-// The work. A call's units of 128 tokens (kv4_plan.h) are divided evenly over
+// The work. A call's units of 256 tokens (kv4_plan.h) are divided evenly over
 // all CTAs, whatever the lengths are. A CTA walks its part; the four warps take
-// 32 tokens each of a unit through rings of their own in shared memory, filled
+// 64 tokens each of a unit through rings of their own in shared memory, filled
 // by asynchronous copies that run ahead across the ends of sequences. At the
 // end of a tile's share the warps' maxima, sums and outputs are joined. A share
 // that is a whole tile is written out; the others go to the workspace, and the
@@ -78,7 +78,7 @@ struct Kv4Attn {
   int few_rows;                 // sequences of up to so many rows a KV head go to the decode
                                 // kernel, the others to the prompt kernel
   int split;                    // tiles may be shared between CTAs
-  int whole;                    // 32 tokens that begin at a multiple of 32 share a page
+  int whole;                    // 64 tokens that begin at a multiple of 64 share a page
   float *ws;                    // the shares (kv4_decode_cfg)
   Kv4Magic magic;
 };
@@ -101,15 +101,15 @@ __device__ __forceinline__ float kv4_down(int e) {
 namespace kv4_decode_cfg {
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
-constexpr int kTok = 32;        // tokens per warp and stage
+constexpr int kTok = 64;        // tokens per warp and stage
 constexpr int kStages = 2;
 constexpr uint32_t kCodeBytes = kTok * 64;
 constexpr uint32_t kStage = 2 * kCodeBytes + 2 * kTok * 4;   // keys, values, their scales
 constexpr uint32_t kRing = kStages * kStage;                 // per warp
 constexpr int kORow = 132;      // floats of an output row in shared memory
-constexpr uint32_t smem_bytes(int nt) {
-  return kWarps * kRing + kWarps * 8 * nt * (kORow + 2) * 4;
-}
+constexpr uint32_t kSmemBytes = kWarps * kRing;
+// The warps' shares of a tile are joined in the stages that its last unit left.
+static_assert(8 * 2 * (kORow + 2) * 4 <= kStage, "a share of 16 rows fits a stage");
 // Workspace: for each CTA two slots of 8 nt rows (128 outputs, maximum, sum),
 // then a descriptor {first CTA, sequence, head, tile} of the tile that ends in
 // it and began in an earlier CTA (first CTA = -1: none).
@@ -124,6 +124,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -208,12 +214,12 @@ struct Kv4Line {
   int b;
 };
 
-// Finds place_of(total) (negative: none). Every thread of the CTA calls it;
-// each sums a run of the sequences.
-template <int kWarps, class Weight, class Place>
+// Finds place_of(total, tiles) (negative: none), `tiles` the sum of tiles_of.
+// Every thread of the CTA calls it; each sums a run of the sequences.
+template <int kWarps, class Weight, class Tiles, class Place>
 __device__ __forceinline__ Kv4Line kv4_find_place(const Kv4Seqs &seqs, const Weight &weight_of,
-                                                  const Place &place_of) {
-  __shared__ int64_t warp_sums[kWarps];
+                                                  const Tiles &tiles_of, const Place &place_of) {
+  __shared__ int64_t warp_sums[kWarps], warp_tiles[kWarps];
   __shared__ int64_t found_rest;
   __shared__ int found_b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -221,12 +227,16 @@ __device__ __forceinline__ Kv4Line kv4_find_place(const Kv4Seqs &seqs, const Wei
   const int64_t run_lo = static_cast<int64_t>(threadIdx.x) * run;
   const int b_lo = run_lo < seqs.batch ? static_cast<int>(run_lo) : seqs.batch;
   const int b_hi = seqs.batch - b_lo < run ? seqs.batch : b_lo + run;
-  int64_t mine = 0;
+  int64_t mine = 0, tiles = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const Kv4Seq s = kv4_load_seq(seqs, b);
     if (!s.ok && blockIdx.x == 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
     mine += weight_of(s);
+    tiles += tiles_of(s);
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+  if (lane == 0) warp_tiles[warp] = tiles;
   int64_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -236,12 +246,14 @@ __device__ __forceinline__ Kv4Line kv4_find_place(const Kv4Seqs &seqs, const Wei
   if (lane == 31) warp_sums[warp] = upto;
   __syncthreads();
   Kv4Line line{0, 0, -1};
+  tiles = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) upto += warp_sums[w];
     line.total += warp_sums[w];
+    tiles += warp_tiles[w];
   }
-  const int64_t place = place_of(line.total);   // the same for the whole CTA
+  const int64_t place = place_of(line.total, tiles);   // the same for the whole CTA
   if (place < 0) return line;
   if (place >= upto - mine && place < upto) {
     int64_t rest = place - (upto - mine);
@@ -267,12 +279,14 @@ struct Kv4Part {
   int parts, b;
 };
 
-template <int kWarps, class Weight>
-__device__ __forceinline__ Kv4Part kv4_find_part(const Kv4Seqs &seqs, const Weight &weight_of) {
+template <int kWarps, class Weight, class Tiles>
+__device__ __forceinline__ Kv4Part kv4_find_part(const Kv4Seqs &seqs, const Weight &weight_of,
+                                                 const Tiles &tiles_of) {
   Kv4Part part{};
   const int cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
-  const Kv4Line line = kv4_find_place<kWarps>(seqs, weight_of, [&](int64_t total) -> int64_t {
-    part.parts = total < ctas ? static_cast<int>(total) : ctas;
+  const Kv4Line line = kv4_find_place<kWarps>(seqs, weight_of, tiles_of, [&](int64_t total,
+                                                                             int64_t tiles) -> int64_t {
+    part.parts = kv4_parts(total, tiles, ctas);
     if (cta >= part.parts) return -1;
     part.begin = kv4_part_begin(total, part.parts, cta);
     part.count = kv4_part_begin(total, part.parts, cta + 1) - part.begin;
@@ -344,13 +358,11 @@ __device__ __forceinline__ void kv4_write_row(const Kv4Attn &p, int64_t row, int
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kv4_decode_cfg::kThreads, NT == 1 ? 4 : 3)
+__global__ void __launch_bounds__(kv4_decode_cfg::kThreads, NT == 1 ? 3 : 2)
 kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
   using namespace kv4_decode_cfg;
   constexpr int R = 8 * NT;
   extern __shared__ __align__(16) uint8_t kv4_smem[];
-  float *o_sm = reinterpret_cast<float *>(kv4_smem + kWarps * kRing);   // [warp][row][kORow]
-  float *ml_sm = o_sm + kWarps * R * kORow;                         // [warp][row][2]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cta = static_cast<int>(blockIdx.x);
@@ -358,11 +370,13 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
   grid_dependency_wait();
 
   // ---- this CTA's part of the line
-  auto weight = [&](const Kv4Seq &q) -> int64_t {
-    return static_cast<int64_t>(kv4_own_tiles(q, p, R)) * p.geom.heads *
-           (p.split ? kv4_units(q.len) : 1);
+  auto tiles = [&](const Kv4Seq &q) -> int64_t {
+    return static_cast<int64_t>(kv4_own_tiles(q, p, R)) * p.geom.heads;
   };
-  const Kv4Part part = kv4_find_part<kWarps>(p.seqs, weight);
+  auto weight = [&](const Kv4Seq &q) -> int64_t {
+    return tiles(q) * (p.split ? kv4_units(q.len) : 1);
+  };
+  const Kv4Part part = kv4_find_part<kWarps>(p.seqs, weight, tiles);
   int *desc = p.split ? reinterpret_cast<int *>(p.ws + gridDim.x * 2 * slot_floats(NT)) + 4 * cta
                       : nullptr;
   if (part.count == 0) {
@@ -400,13 +414,13 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
   const int64_t lane_scale = static_cast<int64_t>(lane) * p.geom.token_stride;
   const int64_t lane_code = static_cast<int64_t>(g) * p.geom.token_stride * 64 + t * 16;
   const int64_t step = static_cast<int64_t>(p.geom.token_stride) * 512;
-  int page_no, page;   // of the next stage's first token, or (not whole) of token `lane`
+  int page_no, page;   // of the next stage's first token (whole)
   auto fetch_page = [&]() {
-    const int pos = lw.unit * kKv4Unit + warp * kTok + (p.whole ? 0 : lane);
+    const int pos = lw.unit * kKv4Unit + warp * kTok;
     page_no = kv4_div(pos, p.geom.by_page);
     page = pos < l_end ? __ldg(p.seqs.table + lw.b * p.seqs.table_stride + page_no) : -1;
   };
-  fetch_page();
+  if (p.whole) fetch_page();
   auto issue = [&](int stage) {
     if (to_load > 0) {
       const int pos0 = lw.unit * kKv4Unit + warp * kTok;
@@ -422,9 +436,14 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
           vec = 0;
           n = 0;
         }
-        const int64_t scale = vec + (lane < n ? lane_scale : 0);
-        cp_async_4z(s_dst + at, p.ks + scale, lane < n ? 4u : 0u);
-        cp_async_4z(s_dst + at + kTok * 4, p.vs + scale, lane < n ? 4u : 0u);
+#pragma unroll
+        for (int i = 0; i < kTok; i += 32) {
+          const bool is = i + lane < n;
+          const int64_t scale =
+              vec + (is ? lane_scale + static_cast<int64_t>(i) * p.geom.token_stride : 0);
+          cp_async_4z(s_dst + at + i * 4, p.ks + scale, is ? 4u : 0u);
+          cp_async_4z(s_dst + at + (kTok + i) * 4, p.vs + scale, is ? 4u : 0u);
+        }
         const uint8_t *kp = p.k4 + lane_code + vec * 64, *vp = p.v4 + lane_code + vec * 64;
         if (n >= kTok) {
 #pragma unroll
@@ -443,22 +462,26 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
           }
         }
       } else {
-        const int pos = pos0 + lane;
-        int64_t vec = -1;
-        if (pos < l_end) {
-          vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, lw.head);
-          if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
-        }
-        const int64_t safe = vec < 0 ? 0 : vec;
-        cp_async_4z(s_dst + at, p.ks + safe, vec < 0 ? 0u : 4u);
-        cp_async_4z(s_dst + at + kTok * 4, p.vs + safe, vec < 0 ? 0u : 4u);
+        for (int j = 0; j < kTok; j += 32) {
+          const int pos = pos0 + j + lane;
+          int64_t vec = -1;
+          if (pos < l_end) {
+            const int no = kv4_div(pos, p.geom.by_page);
+            vec = kv4_vector(p.geom, __ldg(p.seqs.table + lw.b * p.seqs.table_stride + no),
+                             pos - no * p.geom.page_size, lw.head);
+            if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
+          }
+          const int64_t safe = vec < 0 ? 0 : vec;
+          cp_async_4z(s_dst + at + j * 4, p.ks + safe, vec < 0 ? 0u : 4u);
+          cp_async_4z(s_dst + at + (kTok + j) * 4, p.vs + safe, vec < 0 ? 0u : 4u);
 #pragma unroll
-        for (int i = 0; i < kTok / 8; ++i) {
-          const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
-          const int64_t off = (v < 0 ? 0 : v) * 64 + t * 16;
-          const uint32_t bytes = v < 0 ? 0u : 16u;
-          cp_async_16(k_dst + at + i * 512, p.k4 + off, bytes);
-          cp_async_16(v_dst + at + i * 512, p.v4 + off, bytes);
+          for (int i = 0; i < 4; ++i) {
+            const int64_t v = __shfl_sync(0xffffffffu, vec, 8 * i + g);
+            const int64_t off = (v < 0 ? 0 : v) * 64 + t * 16;
+            const uint32_t bytes = v < 0 ? 0u : 16u;
+            cp_async_16(k_dst + at + j * 64 + i * 512, p.k4 + off, bytes);
+            cp_async_16(v_dst + at + j * 64 + i * 512, p.v4 + off, bytes);
+          }
         }
       }
       const bool last = lw.unit + 1 >= lw.units;
@@ -470,7 +493,7 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
         } else {
           ++lw.unit;
         }
-        fetch_page();
+        if (p.whole) fetch_page();
       }
     }
     cp_async_commit();
@@ -520,10 +543,10 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
       if (tok0 < end) {
         const uint8_t *st = ring + stage * kStage;
         const float *sc = reinterpret_cast<const float *>(st + 2 * kCodeBytes);
-        // scores of 32 tokens: rows g and g + 8 of two 16-token halves
-        float x[NT][2][4];
+        // scores of 64 tokens: rows g and g + 8 of four times 16
+        float x[NT][kTok / 16][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kTok / 16; ++h) {
           const uint4 ka = *reinterpret_cast<const uint4 *>(st + (16 * h + g) * 64 + t * 16);
           const uint4 kb = *reinterpret_cast<const uint4 *>(st + (16 * h + g + 8) * 64 + t * 16);
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
@@ -558,12 +581,13 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kTok / 16; ++h)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 if (tok0 + 16 * h + g + 8 * (e >> 1) >= limit[n][e & 1]) x[n][h][e] = -INFINITY;
         }
-        const int e = kv4_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(sc[kTok + lane])));
+        const int e = kv4_exponent(__reduce_max_sync(
+            0xffffffffu, __float_as_uint(fmaxf(sc[kTok + lane], sc[kTok + 32 + lane]))));
         const float ef = static_cast<float>(e), down = kv4_down(e);
         // the references of the columns
         float mx[NT][2];
@@ -572,7 +596,9 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float v = fmaxf(fmaxf(x[n][0][c], x[n][0][c + 2]), fmaxf(x[n][1][c], x[n][1][c + 2]));
+            float v = fmaxf(x[n][0][c], x[n][0][c + 2]);
+#pragma unroll
+            for (int h = 1; h < kTok / 16; ++h) v = max3(v, x[n][h][c], x[n][h][c + 2]);
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -600,19 +626,21 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
         for (int n = 0; n < NT; ++n) {
           const float add[2] = {ef + kKv4Raise - m[n][0], ef + kKv4Raise - m[n][1]};
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < kTok / 16; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[n][h][i] = exp2_approx(x[n][h][i] + add[i & 1]);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float step = (x[n][0][c] + x[n][0][c + 2]) + (x[n][1][c] + x[n][1][c + 2]);
+            float step = 0.f;
+#pragma unroll
+            for (int h = 0; h < kTok / 16; ++h) step += x[n][h][c] + x[n][h][c + 2];
             l[n][c] = fmaf(step, exp2_approx(-ef - kKv4Raise), l[n][c]);
           }
         }
         const uint8_t *vt = st + kCodeBytes + (4 * (t >> 1) + (t & 1)) * 64 +
                             (((g >> 1) ^ (t & 2)) << 4) + ((g & 1) << 3);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kTok / 16; ++h) {
           const float v0 = sc[kTok + 16 * h + g] * down, v1 = sc[kTok + 16 * h + g + 8] * down;
           // weights times value scales, as B operands
           uint32_t wf[NT][2];
@@ -644,12 +672,14 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
         }
       }
       __syncwarp();
-      issue(stage);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (u + 1 < count) {
+        issue(stage);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+      }
     }
 
-    // ---- join the warps' shares
-    __syncthreads();   // the previous share's readers are done
+    // ---- join the warps' shares, each in the stage that it left last
+    float *share = reinterpret_cast<float *>(kv4_smem + warp * kRing + stage * kStage);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -660,11 +690,11 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int r = 8 * n + 2 * t + c;
         if (g == 0) {
-          ml_sm[(warp * R + r) * 2] = m[n][c];
-          ml_sm[(warp * R + r) * 2 + 1] = sum;
+          share[R * kORow + 2 * r] = m[n][c];
+          share[R * kORow + 2 * r + 1] = sum;
         }
         // o[n][i][c], o[n][i][c + 2]: elements 16 g + 2 i, + 1
-        float *dst = o_sm + (warp * R + r) * kORow + 16 * g;
+        float *dst = share + r * kORow + 16 * g;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4 *>(dst + 4 * i) =
@@ -672,19 +702,23 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
                           o[n][2 * i + 1][c + 2]);
       }
     __syncthreads();
+    auto share_of = [&](int w) {
+      return reinterpret_cast<const float *>(kv4_smem + w * kRing + stage * kStage);
+    };
     const bool whole = starts && ends;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = 8 * n + static_cast<int>(threadIdx.x >> 4), d = (threadIdx.x & 15) * 8;
       float top = kKv4NoMax;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml_sm[(w * R + r) * 2]);
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, share_of(w)[R * kORow + 2 * r]);
       float sum = 0.f, acc[8] = {};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_approx(ml_sm[(w * R + r) * 2] - top);
-        sum += f * ml_sm[(w * R + r) * 2 + 1];
-        const float *src = o_sm + (w * R + r) * kORow + d;
+        const float *theirs = share_of(w);
+        const float f = exp2_approx(theirs[R * kORow + 2 * r] - top);
+        sum += f * theirs[R * kORow + 2 * r + 1];
+        const float *src = theirs + r * kORow + d;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += f * src[e];
       }
@@ -704,7 +738,12 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
     if (ends && !starts && threadIdx.x == 0)   // only the first share of a part can
       ended = make_int4(kv4_part_of(part.total, part.parts, part.begin - cw.unit), cw.b, cw.head, cw.tile);
     left -= p.split ? count : 1;
-    if (left > 0) kv4_next_tile<NT>(cw, p);
+    if (left > 0) {
+      __syncthreads();   // the shares have been read
+      issue(stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      kv4_next_tile<NT>(cw, p);
+    }
   }
   if (desc != nullptr && threadIdx.x == 0) *reinterpret_cast<int4 *>(desc) = ended;
 }

@@ -238,12 +238,6 @@ __device__ __forceinline__ Kv4Item kv4_prompt_item(const Kv4Attn &p, int &b, int
   return it;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // A row's scores of a KV tile in the exponent's units (x, -infinity where the
 // row does not see), and the largest, each plus its e: what the reference
 // follows. `sc`, in shared memory: ks, vs (scaled by 2^-e) and the e's, one per
@@ -377,7 +371,8 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   grid_dependency_wait();
   const Kv4Line line = kv4_find_place<kThreads / 32>(
       p.seqs, [&](const Kv4Seq &s) { return kv4_prompt_weight(s, p); },
-      [](int64_t total) -> int64_t {
+      [](const Kv4Seq &) { return 0; },
+      [](int64_t total, int64_t) -> int64_t {
         return blockIdx.x < total ? static_cast<int64_t>(blockIdx.x) : -1;
       });
   tc_fence_before_sync();

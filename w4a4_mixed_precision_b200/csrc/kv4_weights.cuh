@@ -86,9 +86,10 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
   __shared__ __align__(16) uint8_t ring_all[kSmemBytes];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   grid_dependency_wait();
-  const Kv4Part part = kv4_find_part<kWarps>(p.seqs, [&](const Kv4Seq &s) -> int64_t {
-    return static_cast<int64_t>(kv4_wdecode_units(s, p)) * p.geom.heads;
-  });
+  const Kv4Part part = kv4_find_part<kWarps>(
+      p.seqs,
+      [&](const Kv4Seq &s) { return static_cast<int64_t>(kv4_wdecode_units(s, p)) * p.geom.heads; },
+      [&](const Kv4Seq &s) { return kv4_wdecode_units(s, p) > 0 ? p.geom.heads : 0; });
   if (part.count == 0) return;
   Kv4WUnit u;    // what is computed
   u.b = part.b;
@@ -424,7 +425,8 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
   grid_dependency_wait();
   const Kv4Line line = kv4_find_place<kThreads / 32>(
       p.seqs, [&](const Kv4Seq &s) { return kv4_wprompt_weight(s, p); },
-      [](int64_t total) -> int64_t {
+      [](const Kv4Seq &) { return 0; },
+      [](int64_t total, int64_t) -> int64_t {
         return blockIdx.x < total ? static_cast<int64_t>(blockIdx.x) : -1;
       });
   tc_fence_before_sync();
