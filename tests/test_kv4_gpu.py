@@ -239,6 +239,9 @@ def test_attention_weights(new, lens, q_heads, heads, page, causal):
     ([700, 701], 512, 0, 16, 1, False),
     ([2000, 3], 1999, 1, 100, 64, True),
     ([1500], 1, 1, 64, 64, False),
+    ([40000], 3000, 500, 64, 16, False),
+    ([9000, 33], 8999, 0, 24, 64, True),
+    ([0, 20000], 4096, 4096, 16, 100, False),
 ])
 def test_evict_matches_the_oracle(lens, budget, recent, page, to_page, token_major):
     heads = 3

@@ -7,8 +7,9 @@
 // table[b][position / page_size].
 //
 // Both kernels stream: 8 lanes own one vector (16 elements each), as the
-// contiguous cache kernels do. Every team finds its token's sequence by a
-// binary search of cu_q.
+// contiguous cache kernels do, and a warp 16 vectors of a token at once (four a
+// lane), so that a token's sequence (a binary search of cu_q) and page are
+// looked up once for all of them and the loads overlap.
 #pragma once
 
 #include "kv.cuh"
@@ -36,9 +37,9 @@ __device__ __forceinline__ int kv4_sequence_of(const Kv4Seqs &s, int row) {
   return lo;
 }
 
-// Vector number of (row, head)'s slot, or -1 where there is none; what the
+// Vector number of head 0 in the row's slot, or -1 where there is none; what the
 // device arrays get wrong is recorded in the status word.
-__device__ __forceinline__ int64_t kv4_row_vector(const Kv4Rows &p, int row, int head) {
+__device__ __forceinline__ int64_t kv4_row_vector(const Kv4Rows &p, int row) {
   const Kv4Seqs &q = p.seqs;
   const int b = kv4_sequence_of(q, row);
   const int q0 = __ldg(q.cu_q + b), q1 = __ldg(q.cu_q + b + 1);
@@ -51,43 +52,69 @@ __device__ __forceinline__ int64_t kv4_row_vector(const Kv4Rows &p, int row, int
   const int pos = s.len - s.qn + row - q0;
   const int page_no = kv4_div(pos, p.geom.by_page);
   const int page = __ldg(q.table + b * q.table_stride + page_no);
-  const int64_t vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, head);
+  const int64_t vec = kv4_vector(p.geom, page, pos - page_no * p.geom.page_size, 0);
   if (vec < 0) report_status(1 /* ATOM_ERR_INVALID_ARG */);
   return vec;
 }
 
+constexpr int kKv4RowVecs = 16;   // of a row, per warp
+
 template <bool kAppend>
 __global__ void __launch_bounds__(kKvThreads) kv4_rows_kernel(const Kv4Rows p) {
-  const int lane = threadIdx.x & 31, sub = lane & 7;
-  const unsigned team_mask = 0xFFu << (8 * (lane >> 3));
+  const int lane = threadIdx.x & 31, sub = lane & 7, team = lane >> 3;
+  const unsigned team_mask = 0xFFu << (8 * team);
   const int heads = p.geom.heads;
-  const int64_t items = static_cast<int64_t>(p.seqs.rows) * heads * 2;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 3);
-  for (int64_t it = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3; it < items;
-       it += stride) {
-    const int row = static_cast<int>(it / (2 * heads));
-    const int r = static_cast<int>(it - static_cast<int64_t>(row) * (2 * heads));
-    const bool value = r >= heads;
-    const int head = value ? r - heads : r;
-    const int64_t vec = kv4_row_vector(p, row, head);
-    if (vec < 0) continue;   // the same for the team's 8 lanes
-    __half *x = (value ? p.v + row * p.v_token + head * p.v_head
-                       : p.k + row * p.k_token + head * p.k_head) + sub * 16;
-    uint8_t *q4 = (value ? p.v4 : p.k4) + vec * 64 + sub * 8;
-    float *sc = (value ? p.vs : p.ks) + vec;
-    if constexpr (kAppend) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x));
-      const uint4 b = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      float scale;
-      *reinterpret_cast<uint2 *>(q4) = kv_encode16(w, team_mask, scale);
-      if (sub == 0) *sc = scale;
-    } else {
-      uint32_t o[8];
-      kv_decode16(__ldg(reinterpret_cast<const uint2 *>(q4)), __ldg(sc), o);
-      uint4 *dst = reinterpret_cast<uint4 *>(x);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  const int warps = static_cast<int>(gridDim.x) * (kKvThreads / 32);
+  grid_dependency_wait();
+  for (int64_t row64 = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5); row64 < p.seqs.rows;
+       row64 += warps) {
+    const int row = static_cast<int>(row64);
+    const int64_t vec0 = kv4_row_vector(p, row);
+    if (vec0 < 0) continue;
+    // keys of all heads, then values of all heads
+    for (int64_t first = blockIdx.y * kKv4RowVecs; first < 2 * static_cast<int64_t>(heads);
+         first += gridDim.y * kKv4RowVecs) {
+      uint4 a[4], b[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = first + 4 * u + team;
+        const bool value = i >= heads;
+        const int head = static_cast<int>(value ? i - heads : i);
+        if (i >= 2 * static_cast<int64_t>(heads)) continue;   // the same for a team's lanes
+        if constexpr (kAppend) {
+          const __half *x = (value ? p.v + row * p.v_token + head * p.v_head
+                                   : p.k + row * p.k_token + head * p.k_head) + sub * 16;
+          a[u] = __ldg(reinterpret_cast<const uint4 *>(x));
+          b[u] = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
+        } else {
+          const int64_t vec = vec0 + static_cast<int64_t>(head) * p.geom.head_stride;
+          const uint2 q = __ldg(reinterpret_cast<const uint2 *>((value ? p.v4 : p.k4) + vec * 64 + sub * 8));
+          a[u] = make_uint4(q.x, q.y, __float_as_uint(__ldg((value ? p.vs : p.ks) + vec)), 0u);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = first + 4 * u + team;
+        const bool value = i >= heads;
+        const int head = static_cast<int>(value ? i - heads : i);
+        if (i >= 2 * static_cast<int64_t>(heads)) continue;
+        if constexpr (kAppend) {
+          const int64_t vec = vec0 + static_cast<int64_t>(head) * p.geom.head_stride;
+          const uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
+          float scale;
+          *reinterpret_cast<uint2 *>((value ? p.v4 : p.k4) + vec * 64 + sub * 8) =
+              kv_encode16(w, team_mask, scale);
+          if (sub == 0) (value ? p.vs : p.ks)[vec] = scale;
+        } else {
+          uint32_t o[8];
+          kv_decode16(make_uint2(a[u].x, a[u].y), __uint_as_float(a[u].z), o);
+          uint4 *dst = reinterpret_cast<uint4 *>(
+              (value ? p.v + row * p.v_token + head * p.v_head
+                     : p.k + row * p.k_token + head * p.k_head) + sub * 16);
+          dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
     }
   }
 }

@@ -22,6 +22,27 @@ atom_status_t kv4_check_cache(const atom_kv4_cache_t *c, bool touched) {
   return ATOM_OK;
 }
 
+// Whether two runs of memory share a byte.
+bool kv4_overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+}
+bool kv4_caches_overlap(const atom_kv4_cache_t *a, const atom_kv4_cache_t *b) {
+  auto vectors = [](const atom_kv4_cache_t *c) {
+    return c->pages < 1 ? 0 : (c->pages - 1) * c->page_stride + (c->page_size - 1) * c->token_stride +
+                                  (c->heads - 1) * c->head_stride + 1;
+  };
+  const int64_t x = vectors(a), y = vectors(b);
+  const struct { const void *p; int64_t bytes; } src[4] = {
+      {a->k4, x * 64}, {a->v4, x * 64}, {a->ks, x * 4}, {a->vs, x * 4}};
+  const struct { const void *p; int64_t bytes; } dst[4] = {
+      {b->k4, y * 64}, {b->v4, y * 64}, {b->ks, y * 4}, {b->vs, y * 4}};
+  for (const auto &s : src)
+    for (const auto &d : dst)
+      if (kv4_overlap(s.p, s.bytes, d.p, d.bytes)) return true;
+  return false;
+}
+
 atom_status_t kv4_check_table(const int32_t *table, int64_t stride, int64_t max_pages) {
   if (max_pages < 0 || stride < 0) return ATOM_ERR_INVALID_ARG;
   if (stride < max_pages) return ATOM_ERR_SHAPE;
@@ -77,6 +98,24 @@ atomk::Kv4Seqs kv4_seqs(const atom_kv4_batch_t *b, const atom_kv4_cache_t *c, in
   return s;
 }
 
+// Launch that may overlap the end of the kernel before it in the stream (the
+// kernel waits for that one before it touches memory).
+template <class... P>
+cudaError_t kv4_launch(void (*fn)(P...), dim3 grid, int threads, size_t smem,
+                       atom_stream_t stream, const P &...p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p...);
+}
+
 atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_head, const void *v,
                        int64_t v_token, int64_t v_head, int64_t rows, const atom_kv4_cache_t *cache,
                        const atom_kv4_batch_t *batch, atom_stream_t stream) {
@@ -104,13 +143,18 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
   p.k_head = k_head;
   p.v_token = v_token;
   p.v_head = v_head;
-  const int grid = kv_grid(dev, rows * cache->heads * 2);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (append)
-    atomk::kv4_rows_kernel<true><<<grid, atomk::kKvThreads, 0, s>>>(p);
-  else
-    atomk::kv4_rows_kernel<false><<<grid, atomk::kKvThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
+  // a warp a row (and 16 of its vectors), eight CTAs an SM
+  const int64_t ctas = (rows + atomk::kKvThreads / 32 - 1) / (atomk::kKvThreads / 32);
+  const int64_t parts = (2 * cache->heads + atomk::kKv4RowVecs - 1) / atomk::kKv4RowVecs;
+  const int64_t cap = static_cast<int64_t>(dev->sm_count) * 8;
+  const int grid_x = static_cast<int>(ctas < cap ? ctas : cap);
+  int64_t grid_y = cap / grid_x;
+  if (grid_y > parts) grid_y = parts;
+  const cudaError_t err =
+      kv4_launch(append ? atomk::kv4_rows_kernel<true> : atomk::kv4_rows_kernel<false>,
+                 dim3(static_cast<unsigned>(grid_x), static_cast<unsigned>(grid_y), 1),
+                 atomk::kKvThreads, 0, stream, p);
+  return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 
 // Largest number of query rows of a KV head that the decode kernel takes where the
@@ -142,24 +186,6 @@ atom_status_t kv4_decode_ctas(DeviceState *dev, int nt, int *ctas) {
   }
   *ctas = dev->kv4_ctas[nt - 1];
   return ATOM_OK;
-}
-
-// Launch that may overlap the end of the kernel before it in the stream (the
-// kernel waits for that one before it touches memory).
-template <class... P>
-cudaError_t kv4_launch(void (*fn)(P...), int grid, int threads, size_t smem,
-                       atom_stream_t stream, const P &...p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, p...);
 }
 
 // Tensor map of fp16 queries [rows][q_heads][128] whose boxes are the rows of as
@@ -416,9 +442,33 @@ atom_status_t atom_kv4_evict(const float *weights, int64_t width, const atom_kv4
   p.kept = kept;
   p.new_weights = new_weights;
   p.new_width = new_width;
-  atomk::kv4_evict_kernel<<<static_cast<int>(batch->batch * cache->heads), atomk::kKv4EvictThreads,
-                            0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
+  p.in_steps = kv4_caches_overlap(cache, dst) ||
+               (new_weights != nullptr &&
+                kv4_overlap(weights, batch->batch * cache->heads * width * 4, new_weights,
+                            batch->batch * cache->heads * new_width * 4));
+  // CTAs a (sequence, head): as many as leave none without an SM of its own, and
+  // at least 2048 of the widest sequence's tokens to each (1 x 65537, 8 heads:
+  // XXX us with one, XXX with eight)
+  const int64_t rows = batch->batch * cache->heads;
+  int64_t tokens = p.seqs.capacity < width ? p.seqs.capacity : width;
+  int cluster = 1;
+  while (cluster < atomk::kv4_evict_cfg::kMaxCluster && rows * cluster * 2 <= dev->sm_count &&
+         tokens >= int64_t(2048) * cluster * 2)
+    cluster *= 2;
+  if (rows * cluster > INT32_MAX) return ATOM_ERR_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster), 1, 1);
+  cfg.blockDim = dim3(atomk::kv4_evict_cfg::kThreads, 1, 1);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, atomk::kv4_evict_kernel, p, cluster) == cudaSuccess ? ATOM_OK
+                                                                                      : ATOM_ERR_CUDA;
 }
 
 }  // extern "C"
