@@ -42,6 +42,7 @@ struct DeviceState {
   std::atomic<bool> kv4_attr[2] = {};   // by query tile (8, 16 rows): publishes kv4_ctas
   std::atomic<bool> kv4_prompt_attr{false};   // shared-memory limits set for the prompt kernels
   std::atomic<bool> kv4_wprompt_attr{false};
+  std::atomic<bool> kv4_evict_attr{false};    // and for the eviction
   int kv4_ctas[2] = {};           // co-resident CTAs of the cache attention kernel
   uint32_t quant_smem_set = 0;
   std::atomic<void *> noalloc_scratch{nullptr};  // device address of g_noalloc_scratch here

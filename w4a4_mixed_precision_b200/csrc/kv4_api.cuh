@@ -456,9 +456,22 @@ atom_status_t atom_kv4_evict(const float *weights, int64_t width, const atom_kv4
          tokens >= int64_t(2048) * cluster * 2)
     cluster *= 2;
   if (rows * cluster > INT32_MAX) return ATOM_ERR_SHAPE;
+  if (!dev->kv4_evict_attr.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(atomk::kv4_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             atomk::kv4_evict_cfg::kKeys * 4 + 16) != cudaSuccess)
+      return ATOM_ERR_CUDA;
+    dev->kv4_evict_attr.store(true, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster), 1, 1);
   cfg.blockDim = dim3(atomk::kv4_evict_cfg::kThreads, 1, 1);
+  // room for the keys of a CTA's share; a share that does not fit is read again
+  // in every pass
+  const int64_t keys = tokens / cluster + 2 * atomk::kv4_evict_cfg::kRun;
+  cfg.dynamicSmemBytes = keys > atomk::kv4_evict_cfg::kKeys
+                             ? 0
+                             : static_cast<size_t>((keys * 4 + 15) / 16 * 16);
+  p.keys = keys > atomk::kv4_evict_cfg::kKeys ? 0 : static_cast<int>(keys);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;

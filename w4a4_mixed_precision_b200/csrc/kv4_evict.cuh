@@ -14,7 +14,7 @@
 // CTAs add up each other's counts through distributed shared memory, and all
 // find the same value. The counts also say how many of each CTA's tokens stay,
 // so that one more pass numbers them in order. Then the cluster moves the
-// vectors, 8 lanes a token.
+// vectors.
 //
 // In place (or where source and destination memory overlap) the move goes in
 // steps: every copy of a step is read before any is written, and a token never
@@ -24,8 +24,6 @@
 // token and head that stays); one long sequence, latency: four passes and a
 // dozen cluster barriers.
 #pragma once
-
-#include <type_traits>
 
 #include "kv4_plan.h"
 #include "ptx.cuh"
@@ -50,6 +48,7 @@ struct Kv4Evict {
   int32_t *kept;             // [batch][heads][budget]
   float *new_weights;        // [batch][heads][new_width], or null
   int64_t new_width;
+  int keys;                  // that the launch's shared memory holds
   int in_steps;              // source and destination memory overlap
 };
 
@@ -59,10 +58,17 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kRun = 8;                  // tokens a thread numbers at once
-constexpr int kMove = kThreads / 8;      // tokens a CTA moves at once
-constexpr int kUnroll = 4;               // ... so many times over, if not in steps
+constexpr int kKeys = 12288;             // keys kept in shared memory, at most
 }  // namespace kv4_evict_cfg
 
+__device__ __forceinline__ int4 ld_shared_cluster_v4s(uint32_t cluster_addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t cluster_addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
@@ -72,7 +78,9 @@ __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t cluster_addr) {
 __global__ void __launch_bounds__(kv4_evict_cfg::kThreads, 2)
 kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
   using namespace kv4_evict_cfg;
-  __shared__ int hist[kBins];
+  extern __shared__ __align__(16) uint8_t kv4_smem[];
+  uint32_t *keys = reinterpret_cast<uint32_t *>(kv4_smem);
+  __shared__ __align__(16) int hist[kBins];
   __shared__ int scan[2][kWarps];
   __shared__ int counts[2];                // larger than, equal to `least` among this CTA's
   __shared__ int found_bin, found_above;
@@ -102,16 +110,39 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
   const int hi = len - lo < share ? len : lo + share;
   const int old_hi = hi < old ? hi : old;   // [lo, old_hi) must earn theirs
 
+  // The keys of [lo, old_hi), read once, where they fit. Loads of a batch are in
+  // flight together.
+  const bool in_smem = old_hi - lo <= p.keys;
+  if (in_smem && want > 0 && want < old) {
+    for (int i0 = lo; i0 < old_hi; i0 += 8 * kThreads) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * kThreads + tid;
+        v[j] = i < old_hi ? w[i] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * kThreads + tid;
+        if (i < old_hi) keys[i - lo] = kv4_weight_key(__float_as_uint(v[j]));
+      }
+    }
+  }
+  auto key_of = [&](int i) {
+    return in_smem ? keys[i - lo] : kv4_weight_key(__float_as_uint(w[i]));
+  };
+
   // ---- the smallest key that stays, and how many of its equals do
-  uint32_t least = 0;    // 0: all equal or above stay
-  int same = old;
-  int above_here = 0, equal_here = old_hi > lo ? old_hi - lo : 0;   // of this CTA's tokens
+  uint32_t least = 0;    // 0: all stay
+  int same = 0;
+  int above_here = old_hi > lo ? old_hi - lo : 0, equal_here = 0;   // of this CTA's tokens
   if (want == 0) {
     least = 0xFFFFFFFFu;   // above every key (the largest is that of +infinity)
-    same = equal_here = 0;
+    above_here = 0;
   } else if (want < old) {
     uint32_t known = 0;
     int need = want;
+    above_here = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
@@ -122,7 +153,7 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
 #pragma unroll 4
       for (int i0 = lo; i0 < old_hi; i0 += kThreads) {
         const int i = i0 + tid;
-        const uint32_t key = i < old_hi ? kv4_weight_key(__float_as_uint(w[i])) : 0u;
+        const uint32_t key = i < old_hi ? key_of(i) : 0u;
         const bool is = i < old_hi && (key & mask) == known;
         const uint32_t bin = is ? (key >> shift) & bins : kBins;
         // one addition for the lanes of a warp that have the same value (most
@@ -133,15 +164,24 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       sync_all();
       // the bin at which the count from above reaches `need`; thread t has the
       // bins kBins - 1 - 4t .. - 3
-      int mine[4], total = 0, own = 0;
+      const int4 here = *reinterpret_cast<const int4 *>(&hist[kBins - 4 - 4 * tid]);
+      int mine[4] = {here.w, here.z, here.y, here.x}, own = 0;
+      if (cluster > 1) {
+        int4 v[kMaxCluster - 1];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = kBins - 1 - 4 * tid - j;
-        mine[j] = hist[at];
-        for (int c = 1; c < cluster; ++c)
-          mine[j] += ld_shared_cluster_s32(cluster_map(&hist[at], (rank + c) % cluster));
-        total += mine[j];
+        for (int c = 1; c < kMaxCluster; ++c)
+          v[c - 1] = c < cluster ? ld_shared_cluster_v4s(cluster_map(&hist[kBins - 4 - 4 * tid],
+                                                                     (rank + c) % cluster))
+                                 : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 1; c < kMaxCluster; ++c) {
+          mine[0] += v[c - 1].w;
+          mine[1] += v[c - 1].z;
+          mine[2] += v[c - 1].y;
+          mine[3] += v[c - 1].x;
+        }
       }
+      const int total = mine[0] + mine[1] + mine[2] + mine[3];
       int upto = total;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -183,6 +223,7 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
 
   // ---- number the tokens that stay: as many as are above `least` before them,
   // and of its equals the first `same`
+  const bool searched = want > 0 && want < old;
   int above_before = 0, equal_before = 0;
   if (cluster > 1) {
     if (tid == 0) {
@@ -203,7 +244,7 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
     for (int j = 0; j < kRun; ++j) {
       const int i = i0 + j;
       if (i >= hi || i >= old) continue;
-      const uint32_t key = kv4_weight_key(__float_as_uint(w[i]));
+      const uint32_t key = searched ? key_of(i) : 1u;   // (all or none of them stay)
       above |= (key > least ? 1u : 0u) << j;
       equal |= (key == least ? 1u : 0u) << j;
     }
@@ -251,75 +292,67 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
   for (int i = new_len + rank * kThreads + tid; i < p.budget; i += cluster * kThreads) kept[i] = -1;
   sync_all();
 
-  // ---- move them: 8 lanes a token, 4 for the key's and 4 for the value's codes
-  const int part = tid & 7;
-  const bool value = part >= 4;
-  const uint8_t *codes = (value ? p.v4 : p.k4) + (part & 3) * 16;
-  uint8_t *to_codes = (value ? p.to_v4 : p.to_k4) + (part & 3) * 16;
-  const float *scales = value ? p.vs : p.ks;
-  float *to_scales = value ? p.to_vs : p.to_ks;
+  // ---- move them. A warp takes 32 tokens at a time: a lane finds the addresses
+  // of one of them (and moves its scales and weight), then 8 lanes move a token's
+  // codes, 4 the key's and 4 the value's. The addresses of the next 32 are looked
+  // up while the codes are on their way.
   float *new_w = p.new_weights == nullptr
                      ? nullptr
                      : p.new_weights + (static_cast<int64_t>(b) * p.geom.heads + head) * p.new_width;
-  const bool has_scale = (part & 3) == 0, has_weight = part == 1 && new_w != nullptr;
-  auto move = [&](auto unroll, int base, auto between) {
-    constexpr int U = decltype(unroll)::value;
-    int from[U], page[U], to_page[U];
-    int64_t dst[U];
-    uint4 c[U];
-    float s[U], weight[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int to = base + u * kMove + (tid >> 3);
-      from[u] = to < new_len ? kept[to] : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int to = base + u * kMove + (tid >> 3);
-      page[u] = to_page[u] = -1;
-      if (from[u] < 0) continue;
-      page[u] = __ldg(p.seqs.table + b * p.seqs.table_stride + kv4_div(from[u], p.geom.by_page));
-      to_page[u] = __ldg(p.to_table + b * p.to_table_stride + kv4_div(to, p.to_geom.by_page));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int to = base + u * kMove + (tid >> 3);
-      dst[u] = -1;
-      c[u] = make_uint4(0u, 0u, 0u, 0u);
-      s[u] = weight[u] = 0.f;
-      if (from[u] < 0) continue;
-      if (has_weight) weight[u] = w[from[u]];
-      const int64_t src = kv4_vector(p.geom, page[u], from[u] - kv4_div(from[u], p.geom.by_page) *
-                                                                    p.geom.page_size, head);
-      dst[u] = kv4_vector(p.to_geom, to_page[u],
-                          to - kv4_div(to, p.to_geom.by_page) * p.to_geom.page_size, head);
-      if (src < 0 || dst[u] < 0) {
-        report_status(1 /* ATOM_ERR_INVALID_ARG */);
-        dst[u] = -1;
-        continue;
-      }
-      c[u] = *reinterpret_cast<const uint4 *>(codes + src * 64);
-      if (has_scale) s[u] = scales[src];
-    }
-    between();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int to = base + u * kMove + (tid >> 3);
-      if (dst[u] >= 0) {
-        *reinterpret_cast<uint4 *>(to_codes + dst[u] * 64) = c[u];
-        if (has_scale) to_scales[dst[u]] = s[u];
-      }
-      if (from[u] >= 0 && has_weight) new_w[to] = weight[u];
-    }
+  const uint8_t *codes = ((lane & 4) != 0 ? p.v4 : p.k4) + (lane & 3) * 16;
+  uint8_t *to_codes = ((lane & 4) != 0 ? p.to_v4 : p.to_k4) + (lane & 3) * 16;
+  const int32_t *table = p.seqs.table + b * p.seqs.table_stride;
+  const int32_t *to_table = p.to_table + b * p.to_table_stride;
+  int from = -1, page_no = 0, to_page_no = 0, page = -1, to_page = -1;
+  auto look_up = [&](int to) {   // token `to` of those that stay
+    from = to < new_len ? kept[to] : -1;
+    if (from < 0) return;
+    page_no = kv4_div(from, p.geom.by_page);
+    to_page_no = kv4_div(to, p.to_geom.by_page);
+    page = __ldg(table + page_no);
+    to_page = __ldg(to_table + to_page_no);
   };
-  if (p.in_steps) {
-    for (int base = 0; base < new_len; base += cluster * kMove) {
-      move(std::integral_constant<int, 1>{}, base + rank * kMove, sync_all);
-      sync_all();
+  // steps: as many warps as the cluster has, 32 tokens each
+  const int step = cluster * kThreads;
+  const int first = (rank * kWarps + warp) * 32 + lane;
+  look_up(first);
+  for (int base = 0; base < new_len; base += step) {
+    const int to = base + first;
+    int64_t src = -1, dst = -1;
+    float ks = 0.f, vs = 0.f, weight = 0.f;
+    const bool mine = from >= 0;
+    if (mine) {
+      src = kv4_vector(p.geom, page, from - page_no * p.geom.page_size, head);
+      dst = kv4_vector(p.to_geom, to_page, to - to_page_no * p.to_geom.page_size, head);
+      if (new_w != nullptr) weight = w[from];
+      if (src < 0 || dst < 0) {
+        report_status(1 /* ATOM_ERR_INVALID_ARG */);
+        src = dst = -1;
+      } else {
+        ks = p.ks[src];
+        vs = p.vs[src];
+      }
     }
-  } else {
-    for (int base = rank * kUnroll * kMove; base < new_len; base += cluster * kUnroll * kMove)
-      move(std::integral_constant<int, kUnroll>{}, base, [] {});
+    uint4 c[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t at = __shfl_sync(0xffffffffu, src, 4 * u + (lane >> 3));
+      c[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at >= 0) c[u] = *reinterpret_cast<const uint4 *>(codes + at * 64);
+    }
+    look_up(to + step);
+    if (p.in_steps) sync_all();   // all of the step's copies have been read
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t at = __shfl_sync(0xffffffffu, dst, 4 * u + (lane >> 3));
+      if (at >= 0) *reinterpret_cast<uint4 *>(to_codes + at * 64) = c[u];
+    }
+    if (dst >= 0) {
+      p.to_ks[dst] = ks;
+      p.to_vs[dst] = vs;
+    }
+    if (mine && new_w != nullptr) new_w[to] = weight;
+    if (p.in_steps) sync_all();   // ... and written
   }
 }
 
