@@ -92,6 +92,10 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
     if (cluster > 1) cluster_sync();
     else __syncthreads();
   };
+  // sum of the values of the warps before this one
+  auto warps_before = [&](const int (&of)[kWarps]) {
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, lane < warp ? of[lane & (kWarps - 1)] : 0));
+  };
   const int len = __ldg(p.seqs.kv_lens + b);
   const int new_len = len < p.budget ? len : p.budget;
   if (len < 0 || len > p.seqs.capacity || len > p.width || new_len > p.to_capacity) {
@@ -150,16 +154,12 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       const uint32_t mask = pass == 0 ? 0u : (pass == 1 ? 0xFFE00000u : 0xFFFFFC00u);
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
       for (int i0 = lo; i0 < old_hi; i0 += kThreads) {
         const int i = i0 + tid;
         const uint32_t key = i < old_hi ? key_of(i) : 0u;
         const bool is = i < old_hi && (key & mask) == known;
-        const uint32_t bin = is ? (key >> shift) & bins : kBins;
-        // one addition for the lanes of a warp that have the same value (most
-        // weights are small, many are zero)
-        const unsigned peers = __match_any_sync(0xffffffffu, bin);
-        if (is && lane == __ffs(peers) - 1) atomicAdd(&hist[bin], __popc(peers));
+        if (is) atomicAdd(&hist[(key >> shift) & bins], 1);
       }
       sync_all();
       // the bin at which the count from above reaches `need`; thread t has the
@@ -190,7 +190,7 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       }
       if (lane == 31) scan[0][warp] = upto;
       __syncthreads();
-      for (int v = 0; v < warp; ++v) upto += scan[0][v];
+      upto += warps_before(scan[0]);
       int above = upto - total;
       if (above < need && upto >= need) {
 #pragma unroll
@@ -213,7 +213,7 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       own = __reduce_add_sync(0xffffffffu, own);
       if (lane == 0) scan[1][warp] = own;
       __syncthreads();
-      for (int v = 0; v < kWarps; ++v) above_here += scan[1][v];
+      above_here += __reduce_add_sync(0xffffffffu, lane < kWarps ? scan[1][lane] : 0);
       equal_here = hist[bin];
       sync_all();   // the counts have been read
     }
@@ -237,16 +237,29 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
     }
   }
 #pragma unroll 1
-  for (int base = lo; base < hi; base += kThreads * kRun) {
+  for (int base = lo; base < old_hi; base += kThreads * kRun) {
     const int i0 = base + tid * kRun;
     unsigned above = 0, equal = 0;   // bits: tokens i0 ..
+    uint32_t run[kRun];
+    if (searched && in_smem && i0 + kRun <= old_hi) {   // (lo and i0 are multiples of kRun apart)
+#pragma unroll
+      for (int j = 0; j < kRun; j += 4) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(keys + i0 - lo + j);
+        run[j] = k.x;
+        run[j + 1] = k.y;
+        run[j + 2] = k.z;
+        run[j + 3] = k.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRun; ++j)   // (without a search all or none of them stay)
+        run[j] = searched && i0 + j < old_hi ? key_of(i0 + j) : 1u;
+    }
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const int i = i0 + j;
-      if (i >= hi || i >= old) continue;
-      const uint32_t key = searched ? key_of(i) : 1u;   // (all or none of them stay)
-      above |= (key > least ? 1u : 0u) << j;
-      equal |= (key == least ? 1u : 0u) << j;
+      if (i0 + j >= old_hi) continue;
+      above |= (run[j] > least ? 1u : 0u) << j;
+      equal |= (run[j] == least ? 1u : 0u) << j;
     }
     const int mine_a = __popc(above), mine_e = __popc(equal);
     int a = mine_a, e = mine_e;
@@ -263,32 +276,20 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       scan[1][warp] = e;
     }
     __syncthreads();
-    a += above_before - mine_a;
-    e += equal_before - mine_e;
-    for (int v = 0; v < kWarps; ++v) {
-      if (v < warp) {
-        a += scan[0][v];
-        e += scan[1][v];
-      }
-      above_before += scan[0][v];
-      equal_before += scan[1][v];
-    }
+    a += above_before - mine_a + warps_before(scan[0]);
+    e += equal_before - mine_e + warps_before(scan[1]);
+    above_before += __reduce_add_sync(0xffffffffu, lane < kWarps ? scan[0][lane] : 0);
+    equal_before += __reduce_add_sync(0xffffffffu, lane < kWarps ? scan[1][lane] : 0);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const int i = i0 + j;
-      if (i >= hi) continue;
-      if (i >= old) {
-        kept[want + i - old] = i;
-      } else if ((above >> j) & 1u) {
-        kept[a + (e < same ? e : same)] = i;
-        ++a;
-      } else if ((equal >> j) & 1u) {
-        if (e < same) kept[a + e] = i;
-        ++e;
-      }
+      const int is_above = (above >> j) & 1, is_equal = (equal >> j) & 1;
+      if (is_above | (is_equal & (e < same ? 1 : 0))) kept[a + (e < same ? e : same)] = i0 + j;
+      a += is_above;
+      e += is_equal;
     }
   }
+  for (int i = old + rank * kThreads + tid; i < len; i += cluster * kThreads) kept[want + i - old] = i;
   for (int i = new_len + rank * kThreads + tid; i < p.budget; i += cluster * kThreads) kept[i] = -1;
   sync_all();
 
