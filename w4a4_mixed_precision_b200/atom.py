@@ -148,7 +148,7 @@ def _valid_k(K: int) -> bool:
 
 
 def _expect_shape(t: torch.Tensor, shape, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -635,32 +635,22 @@ class KV4Batch:
         self._ref = ct.addressof(self.struct)
 
 
-class _kv4_call:
-    """Runs a call on `device`: makes it the current device, and the call's stream (default:
-    the device's current one) the one whose memory new tensors come from."""
-
-    def __init__(self, device: torch.device, stream):
-        self.device, self.stream, self.contexts = device, stream, ()
-
-    def __enter__(self) -> int:
-        if self.stream is None and torch.cuda.current_device() == self.device.index:
-            return torch.cuda.current_stream().cuda_stream
-        if self.stream is None:
-            self.contexts = (torch.cuda.device(self.device),)
-        else:
-            given = self.stream
-            if not hasattr(given, "cuda_stream"):
-                given = torch.cuda.ExternalStream(int(given), device=self.device)
-            if given.device != self.device:
-                raise ValueError(f"the stream is on {given.device}, the tensors on {self.device}")
-            self.contexts = (torch.cuda.device(self.device), torch.cuda.stream(given))
-        for c in self.contexts:
-            c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+def _kv4_run(device: torch.device, stream, call):
+    """call(stream handle) with `device` current and the call's stream (default: the device's
+    current one) the one whose memory new tensors come from."""
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        # the same handle as torch.cuda.current_stream()'s, without the 3 us of its object: a
+        # third of what a call for a few tokens takes
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _kv4_same_device(cache: KV4Cache, batch: KV4Batch) -> torch.device:
@@ -677,9 +667,9 @@ def atom_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, batch: KV
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have the same rows")
     kp, vp = _kv4_rows(k, cache.heads, "k", device), _kv4_rows(v, cache.heads, "v", device)
-    with _kv4_call(device, stream) as s:
-        st = lib().atom_kv4_append(*kp, *vp, k.shape[0], cache._ref, batch._ref, s)
-    _check("atom_kv4_append", st)
+    fn = lib().atom_kv4_append
+    _check("atom_kv4_append", _kv4_run(device, stream, lambda s: fn(
+        *kp, *vp, k.shape[0], cache._ref, batch._ref, s)))
 
 
 def atom_kv4_gather(cache: KV4Cache, batch: KV4Batch, rows: int,
@@ -689,16 +679,15 @@ def atom_kv4_gather(cache: KV4Cache, batch: KV4Batch, rows: int,
     128] with atom_kv_dequant's values. Rows that no sequence has are not written."""
     device = _kv4_same_device(cache, batch)
     shape = (rows, cache.heads, 128)
-    with _kv4_call(device, stream) as s:
-        if k is None:
-            k = torch.empty(shape, dtype=torch.float16, device=device)
-        if v is None:
-            v = torch.empty(shape, dtype=torch.float16, device=device)
-        st = lib().atom_kv4_gather(cache._ref, batch._ref, rows,
-                                   _kv4_contiguous(k, torch.float16, shape, "k", device),
-                                   _kv4_contiguous(v, torch.float16, shape, "v", device), s)
-    _check("atom_kv4_gather", st)
-    return k, v
+
+    def call(s):
+        out = [cache.ks.new_empty(shape, dtype=torch.float16) if t is None else t for t in (k, v)]
+        _check("atom_kv4_gather", lib().atom_kv4_gather(
+            cache._ref, batch._ref, rows,
+            *(_kv4_contiguous(t, torch.float16, shape, n, device) for t, n in zip(out, "kv")), s))
+        return tuple(out)
+
+    return _kv4_run(device, stream, call)
 
 
 def atom_kv4_attention_workspace_bytes(rows: int, q_heads: int, heads: int, max_q: int) -> int:
@@ -720,31 +709,31 @@ def atom_kv4_attention(q: torch.Tensor, cache: KV4Cache, batch: KV4Batch, causal
     device = _kv4_same_device(cache, batch)
     qp = _kv4_rows(q, None, "q", device)
     rows, q_heads = q.shape[0], q.shape[1]
-    with _kv4_call(device, stream) as s:
-        if out is None:
-            out = torch.empty((rows, q_heads, 128), dtype=torch.float16, device=device)
-        if lse is None:
-            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=device)
-        ws_ptr, ws_bytes = None, 0
+    if workspace is not None and split:
+        _kv4_check(workspace, torch.uint8, "workspace", device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+
+    def call(s):
+        o = q.new_empty((rows, q_heads, 128)) if out is None else out
+        z = cache.ks.new_empty((rows, q_heads)) if lse is None else lse
+        ws, ws_bytes = workspace, 0
         if split:
-            if workspace is None:
+            if ws is None:
                 ws_bytes = lib().atom_kv4_attention_workspace_bytes(rows, q_heads, cache.heads,
                                                                     batch.max_q)
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+                ws = cache.k4.new_empty(ws_bytes) if ws_bytes else None
             else:
-                _kv4_check(workspace, torch.uint8, "workspace", device)
-                if not workspace.is_contiguous():
-                    raise ValueError("workspace must be contiguous")
-                ws_bytes = workspace.numel()
-            ws_ptr = workspace.data_ptr() if ws_bytes else None
-        st = lib().atom_kv4_attention(
+                ws_bytes = ws.numel()
+        _check("atom_kv4_attention", lib().atom_kv4_attention(
             *qp, rows, q_heads, cache._ref, batch._ref, 1 if causal else 0,
             128.0 ** -0.5 if scale is None else scale,
-            _kv4_contiguous(out, torch.float16, (rows, q_heads, 128), "out", device),
-            _kv4_contiguous(lse, torch.float32, (rows, q_heads), "lse", device),
-            ws_ptr, ws_bytes, s)
-    _check("atom_kv4_attention", st)
-    return out, lse
+            _kv4_contiguous(o, torch.float16, (rows, q_heads, 128), "out", device),
+            _kv4_contiguous(z, torch.float32, (rows, q_heads), "lse", device),
+            ws.data_ptr() if ws_bytes else None, ws_bytes, s))
+        return o, z
+
+    return _kv4_run(device, stream, call)
 
 
 def atom_kv4_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: KV4Cache,
@@ -766,12 +755,11 @@ def atom_kv4_attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: KV4Cac
     prev_ptr = None
     if prev is not None:
         prev_ptr = _kv4_contiguous(prev, torch.float32, shape, "prev", device)
-    with _kv4_call(device, stream) as s:
-        st = lib().atom_kv4_attention_weights(
-            *qp, rows, q_heads, _kv4_contiguous(lse, torch.float32, (rows, q_heads), "lse", device),
-            cache._ref, batch._ref, 1 if causal else 0, 128.0 ** -0.5 if scale is None else scale,
-            prev_ptr, sums_ptr, width, s)
-    _check("atom_kv4_attention_weights", st)
+    lse_ptr = _kv4_contiguous(lse, torch.float32, (rows, q_heads), "lse", device)
+    fn = lib().atom_kv4_attention_weights
+    _check("atom_kv4_attention_weights", _kv4_run(device, stream, lambda s: fn(
+        *qp, rows, q_heads, lse_ptr, cache._ref, batch._ref, 1 if causal else 0,
+        128.0 ** -0.5 if scale is None else scale, prev_ptr, sums_ptr, width, s)))
     return sums
 
 
@@ -800,20 +788,20 @@ def atom_kv4_evict(weights: torch.Tensor, cache: KV4Cache, batch: KV4Batch, budg
     if to_pages > 1 and to_table.stride(1) != 1:
         raise ValueError("to_table rows must be contiguous")
     lens_ptr = _kv4_contiguous(new_lens, torch.int32, (n,), "new_lens", device)
-    with _kv4_call(device, stream) as s:
-        if kept is None:
-            kept = torch.empty((n, heads, budget), dtype=torch.int32, device=device)
-        if new_weights is None:
-            new_weights = torch.empty((n, heads, budget), dtype=torch.float32, device=device)
-        new_width = new_weights.shape[-1]
-        st = lib().atom_kv4_evict(
+
+    def call(s):
+        at = weights.new_empty((n, heads, budget), dtype=torch.int32) if kept is None else kept
+        w = weights.new_empty((n, heads, budget)) if new_weights is None else new_weights
+        new_width = w.shape[-1]
+        _check("atom_kv4_evict", lib().atom_kv4_evict(
             weights_ptr, width, cache._ref, batch._ref, budget, recent, dst._ref,
             to_table.data_ptr(), to_table.stride(0) if n > 1 else to_pages, to_pages, lens_ptr,
-            _kv4_contiguous(kept, torch.int32, (n, heads, budget), "kept", device),
-            _kv4_contiguous(new_weights, torch.float32, (n, heads, new_width), "new_weights",
-                            device), new_width, s)
-    _check("atom_kv4_evict", st)
-    return kept, new_weights
+            _kv4_contiguous(at, torch.int32, (n, heads, budget), "kept", device),
+            _kv4_contiguous(w, torch.float32, (n, heads, new_width), "new_weights", device),
+            new_width, s))
+        return at, w
+
+    return _kv4_run(device, stream, call)
 
 
 def atom_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
