@@ -184,6 +184,39 @@ def test_value_sizes_that_grow_and_shrink_along_the_sequence(new):
     check_attention(c)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,lens,q_heads,heads,page", [
+    ([200, 1, 0, 129, 128, 127, 17, 300, 113, 112], [200, 30, 9, 700, 128, 127, 0, 300, 2, 500], 6, 6, 16),
+    ([64, 17, 0, 1, 30, 65, 16, 200], [64, 1000, 20, 1, 29, 65, 333, 900], 56, 8, 24),
+    ([3, 2, 5, 1, 4, 7, 0, 3], [3, 100, 60, 64, 4, 300, 5, 0], 480, 5, 7),
+    ([1, 2, 3, 4, 2, 3, 1, 2], [1, 65, 129, 4, 90, 3, 64, 700], 640, 5, 64),
+    ([130] * 8, [1000, 130, 2049, 513, 140, 131, 4000, 191], 16, 8, 100),
+    ([257, 256, 255, 1, 512, 64, 40, 9], [257, 256, 300, 700, 512, 2000, 40, 9], 10, 5, 1),
+])
+def test_many_prompts(new, lens, q_heads, heads, page, causal):
+    """Batches with rows enough for the kernel that reads the cache once per 256 of them."""
+    check_attention(Call(22, new, lens, q_heads=q_heads, heads=heads, page=page, q_size=0.05),
+                    causal=causal)
+
+
+@pytest.mark.parametrize("power", [-20, 13])
+def test_many_prompts_with_values_of_any_size(power):
+    c = Call(23, [200] * 8, [400, 300, 200, 210, 333, 230, 1000, 201], q_heads=8, heads=8, page=16,
+             q_size=0.05, token_major=True)
+    c.cache[3] = (c.cache[3] * np.float32(2.0 ** power) / np.nanmax(c.cache[3])).astype(np.float32)
+    check_attention(c)
+
+
+def test_many_prompts_with_value_sizes_that_grow_and_shrink():
+    c = Call(24, [210] * 8, [1300, 900, 210, 700, 500, 300, 1000, 800], q_heads=8, heads=8, page=16,
+             q_size=0.3)
+    for b, n in enumerate(c.lens):
+        at = np.arange(n)
+        size = np.exp2(18 * np.sin(at / 150.0) - 5)[:, None].astype(np.float32)
+        c.cache[3][c.table[b, at // 16], at % 16] *= size / 8
+    check_attention(c)
+
+
 def test_scale_and_larger_bound_on_new_tokens():
     c = Call(19, [1, 2], [40, 50], page=16, q_size=0.05)
     check_attention(c, scale=0.3)

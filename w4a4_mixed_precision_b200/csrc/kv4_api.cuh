@@ -157,9 +157,25 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
   return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 
-// Largest number of query rows of a KV head that the decode kernel takes where the
-// prompt kernel runs too.
-constexpr int kKv4FewRows = 16;
+// Largest number of query rows of a KV head that goes to the decode kernel where
+// `heads` (sequence, KV head) pairs are in a call; more go to the prompt kernel.
+// The decode kernel reads the cache once per 16 rows and divides that evenly over
+// the GPU: 44 us per million tokens, pair and 16 rows. The prompt kernel reads it
+// once per 256 rows, with one CTA an SM and a CTA a pair and 256 rows: 22 us per
+// thousand tokens for each round of CTAs. (Both measured: 16 sequences of 3000
+// tokens, 8 heads, 64 rows 76 and 77 us, 128 rows 139 and 78; one sequence, 512
+// rows 44 and 73.)
+int64_t kv4_few_rows(int64_t pairs, int sms) {
+  int64_t rows = 16;
+  for (; rows < 4096; rows += 16) {
+    const int64_t rounds = (pairs * ((rows + 16 + 255) / 256) + sms - 1) / sms;
+    if (pairs * ((rows + 16) / 16) >= 500 * rounds) break;
+  }
+  return rows;
+}
+// The same for the attention weights: 64 sequences of 8192 tokens with 8 rows 77
+// us in the first kernel; 16 of 3000, 8 heads, 24 rows 43 and 45, 32 rows 54 and 45.
+constexpr int kKv4WeightFewRows = 24;
 
 // Query rows a CTA of the decode kernel takes at once, 8 or 16: the smallest
 // that holds every sequence's rows of a KV head, so that the cache is read once.
@@ -209,8 +225,8 @@ bool kv4_query_map(CUtensorMap *map, const void *q, int64_t q_token, int64_t q_h
 // than the decode kernel should take, its tokens' rows fit a tile, and a tensor
 // map describes its queries.
 bool kv4_prompt_call(CUtensorMap *map, const void *q, int64_t q_token, int64_t q_head, int64_t rows,
-                     int64_t q_heads, int group, int64_t max_q) {
-  return max_q * group > kKv4FewRows && group <= 128 &&
+                     int64_t q_heads, int group, int64_t max_q, int64_t few_rows) {
+  return max_q * group > few_rows && group <= 128 &&
          kv4_query_map(map, q, q_token, q_head, rows, q_heads, group);
 }
 
@@ -295,14 +311,15 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   // with pages of 16).
   p.whole = cache->page_size % atomk::kv4_decode_cfg::kTok == 0;
   p.max_q = static_cast<int>(batch->max_q < rows ? batch->max_q : rows);
-  // Sequences with up to 16 query rows a KV head go to the decode kernel, those
-  // with more to the prompt kernel; one that no sequence can need is not launched.
+  // Sequences with few query rows a KV head go to the decode kernel, those with
+  // more to the prompt kernel; one that no sequence can need is not launched.
   CUtensorMap q_map;
+  const int64_t few_rows = kv4_few_rows(batch->batch * cache->heads, dev->sm_count);
   const bool prompts =
-      kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, p.max_q);
+      kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, p.max_q, few_rows);
   const bool decode = !prompts || batch->batch > 1;
   p.tile_rows = prompts ? 128 / p.group * p.group : 0;
-  p.few_rows = !prompts ? INT32_MAX : (decode ? kKv4FewRows : 0);
+  p.few_rows = !prompts ? INT32_MAX : (decode ? static_cast<int>(few_rows) : 0);
   cudaError_t err = cudaSuccess;
   if (prompts) {
     using namespace atomk::kv4_prompt_cfg;
@@ -371,10 +388,11 @@ atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t
   // nothing else)
   const int64_t max_q = batch->max_q < rows ? batch->max_q : rows;
   CUtensorMap q_map;
-  const bool prompts = kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, max_q);
+  const bool prompts = kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, max_q,
+                                       kKv4WeightFewRows);
   const bool few = !prompts || batch->batch > 1;
   p.tile_rows = prompts ? 128 / p.group * p.group : 0;
-  p.few_rows = !prompts ? INT32_MAX : (few ? kKv4FewRows : 0);
+  p.few_rows = !prompts ? INT32_MAX : (few ? kKv4WeightFewRows : 0);
   cudaError_t err = cudaSuccess;
   if (prompts) {
     using namespace atomk::kv4_wprompt_cfg;
