@@ -554,6 +554,15 @@ def _kv4_contiguous(t: torch.Tensor, dtype: torch.dtype, shape, name: str, devic
     return t.data_ptr()
 
 
+def _kv4_output(t: Optional[torch.Tensor], like: torch.Tensor, dtype: torch.dtype, shape, name: str,
+                device) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one on `like`'s device."""
+    if t is None:   # (naming a type costs some microseconds)
+        return like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
+    _kv4_contiguous(t, dtype, shape, name, device)
+    return t
+
+
 class KV4Cache:
     """A paged INT4 KV cache (see include/atom.h): codes k4, v4 uint8 [pages, page_size,
     heads, 64] and scales ks, vs float32 [pages, page_size, heads], all on one device, in
@@ -681,10 +690,10 @@ def atom_kv4_gather(cache: KV4Cache, batch: KV4Batch, rows: int,
     shape = (rows, cache.heads, 128)
 
     def call(s):
-        out = [cache.ks.new_empty(shape, dtype=torch.float16) if t is None else t for t in (k, v)]
+        out = [_kv4_output(t, cache.k4, torch.float16, shape, n, device)
+               for t, n in ((k, "k"), (v, "v"))]
         _check("atom_kv4_gather", lib().atom_kv4_gather(
-            cache._ref, batch._ref, rows,
-            *(_kv4_contiguous(t, torch.float16, shape, n, device) for t, n in zip(out, "kv")), s))
+            cache._ref, batch._ref, rows, out[0].data_ptr(), out[1].data_ptr(), s))
         return tuple(out)
 
     return _kv4_run(device, stream, call)
@@ -715,8 +724,8 @@ def atom_kv4_attention(q: torch.Tensor, cache: KV4Cache, batch: KV4Batch, causal
             raise ValueError("workspace must be contiguous")
 
     def call(s):
-        o = q.new_empty((rows, q_heads, 128)) if out is None else out
-        z = cache.ks.new_empty((rows, q_heads)) if lse is None else lse
+        o = _kv4_output(out, q, torch.float16, (rows, q_heads, 128), "out", device)
+        z = _kv4_output(lse, cache.ks, torch.float32, (rows, q_heads), "lse", device)
         ws, ws_bytes = workspace, 0
         if split:
             if ws is None:
@@ -728,9 +737,7 @@ def atom_kv4_attention(q: torch.Tensor, cache: KV4Cache, batch: KV4Batch, causal
         _check("atom_kv4_attention", lib().atom_kv4_attention(
             *qp, rows, q_heads, cache._ref, batch._ref, 1 if causal else 0,
             128.0 ** -0.5 if scale is None else scale,
-            _kv4_contiguous(o, torch.float16, (rows, q_heads, 128), "out", device),
-            _kv4_contiguous(z, torch.float32, (rows, q_heads), "lse", device),
-            ws.data_ptr() if ws_bytes else None, ws_bytes, s))
+            o.data_ptr(), z.data_ptr(), ws.data_ptr() if ws_bytes else None, ws_bytes, s))
         return o, z
 
     return _kv4_run(device, stream, call)
@@ -790,15 +797,14 @@ def atom_kv4_evict(weights: torch.Tensor, cache: KV4Cache, batch: KV4Batch, budg
     lens_ptr = _kv4_contiguous(new_lens, torch.int32, (n,), "new_lens", device)
 
     def call(s):
-        at = weights.new_empty((n, heads, budget), dtype=torch.int32) if kept is None else kept
-        w = weights.new_empty((n, heads, budget)) if new_weights is None else new_weights
-        new_width = w.shape[-1]
+        at = _kv4_output(kept, weights, torch.int32, (n, heads, budget), "kept", device)
+        new_width = budget if new_weights is None else new_weights.shape[-1]
+        w = _kv4_output(new_weights, weights, torch.float32, (n, heads, new_width), "new_weights",
+                        device)
         _check("atom_kv4_evict", lib().atom_kv4_evict(
             weights_ptr, width, cache._ref, batch._ref, budget, recent, dst._ref,
             to_table.data_ptr(), to_table.stride(0) if n > 1 else to_pages, to_pages, lens_ptr,
-            _kv4_contiguous(at, torch.int32, (n, heads, budget), "kept", device),
-            _kv4_contiguous(w, torch.float32, (n, heads, new_width), "new_weights", device),
-            new_width, s))
+            at.data_ptr(), w.data_ptr(), new_width, s))
         return at, w
 
     return _kv4_run(device, stream, call)

@@ -158,16 +158,17 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
 }
 
 // Largest number of query rows of a KV head that goes to the decode kernel where
-// `heads` (sequence, KV head) pairs are in a call; more go to the prompt kernel.
+// a call has `pairs` (sequence, KV head) pairs with up to `max_rows` of them; more
+// go to the prompt kernel.
 // The decode kernel reads the cache once per 16 rows and divides that evenly over
 // the GPU: 44 us per million tokens, pair and 16 rows. The prompt kernel reads it
 // once per 256 rows, with one CTA an SM and a CTA a pair and 256 rows: 22 us per
 // thousand tokens for each round of CTAs. (Both measured: 16 sequences of 3000
 // tokens, 8 heads, 64 rows 76 and 77 us, 128 rows 139 and 78; one sequence, 512
 // rows 44 and 73.)
-int64_t kv4_few_rows(int64_t pairs, int sms) {
+int64_t kv4_few_rows(int64_t pairs, int64_t max_rows, int sms) {
   int64_t rows = 16;
-  for (; rows < 4096; rows += 16) {
+  for (; rows < max_rows && rows < 4096; rows += 16) {
     const int64_t rounds = (pairs * ((rows + 16 + 255) / 256) + sms - 1) / sms;
     if (pairs * ((rows + 16) / 16) >= 500 * rounds) break;
   }
@@ -314,7 +315,8 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   // Sequences with few query rows a KV head go to the decode kernel, those with
   // more to the prompt kernel; one that no sequence can need is not launched.
   CUtensorMap q_map;
-  const int64_t few_rows = kv4_few_rows(batch->batch * cache->heads, dev->sm_count);
+  const int64_t few_rows = kv4_few_rows(batch->batch * cache->heads,
+                                        static_cast<int64_t>(p.max_q) * p.group, dev->sm_count);
   const bool prompts =
       kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, p.max_q, few_rows);
   const bool decode = !prompts || batch->batch > 1;
