@@ -27,9 +27,19 @@
 //   warps 8..11, 12..15  load packed keys and values, expand them to operand tiles
 //   warps 16, 17         issue the MMAs of query tile 0 and 1
 //   warp 18, lane 0      finds the work items, starts the copies of their queries
-// While the tensor core multiplies for one query tile, the other tile's
-// weights are made. What bounds it: the exponentials, 16 per clock and SM (1024
-// clocks per 128x128 tile), as much as the two products (1024 clocks).
+// While the tensor core multiplies for one query tile, the other tile's weights
+// are made. What bounds it: of the clocks of a KV tile and two query tiles, some
+// 2200, the tensor core works 1776 (74 for each instruction of S, 16 x 128 x 64,
+// which its operands' way out of shared memory costs, and 74 for each of O), the
+// exponential unit 1056, and the issue slots are half full. With nearly all
+// products left out it takes 6 per cent less, with the exponentials left out 15:
+// it is the softmax warps' own chain, two of them on each scheduler, that takes
+// the time (alone, a tile's scores take a warp 250 clocks and its weights 630;
+// two warps together 1370). What was tried against it and was not faster: four
+// softmax warps a scheduler with half the columns each (394 us for the 4096-token
+// prompt against 340), weights before the tile's own maximum is known (476), the
+// two warps taking turns at the exponentials (337 against 334), the next tile's
+// scores read ahead (356 against 334).
 //
 // Operand layouts. K and V tiles are 128 rows (tokens) of 256 bytes as two
 // halves of 128-byte rows with the 128-byte swizzle: for S they are a K-major B
@@ -133,14 +143,15 @@ __device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity,
   return false;
 }
 
-// Bounded wait without the timer of mbar_wait_inline (a phase that has completed
-// costs less: 1x4096 prompt 334 -> 332 us): a look takes some tens of cycles, or
-// as long as the hardware suspends the thread.
+// Bounded wait without a timer, which costs the softmax 2 per cent wherever it is
+// read (1x4096 prompt 323 us with it, 315 without): a look takes at least 20
+// clocks, and what is waited for here takes some microseconds. The roles that
+// issue the MMAs wait with a timer, and their giving up ends this wait too.
 __device__ __forceinline__ bool mbar_wait_spin(uint64_t *bar, uint32_t parity,
                                                const volatile int *abort_flag) {
-  for (uint32_t i = 0; i < kWaitLimitNs / 16; ++i) {
+  for (uint32_t i = 1; i <= 1u << 22; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 63u && *abort_flag) return false;
+    if ((i & 63u) == 0 && *abort_flag) return false;
   }
   return false;
 }
@@ -192,15 +203,6 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
   asm("add.rn.f32x2 %0, %1, %2;"
       : "=l"(reinterpret_cast<uint64_t &>(d))
       : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
-  return d;
-}
-
-__device__ __forceinline__ float2 f2_mul_add(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t &>(d))
-      : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
-        "l"(reinterpret_cast<const uint64_t &>(c)));
   return d;
 }
 
@@ -503,7 +505,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             y[k] = make_float2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
-            y[k] = n > 0 ? f2_mul_add(y[k], make_float2(inv, inv), make_float2(0.f, 0.f))
+            y[k] = n > 0 ? f2_fma(y[k], make_float2(inv, inv), make_float2(0.f, 0.f))
                          : make_float2(0.f, 0.f);
           }
           st_shared_v4(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4),

@@ -472,7 +472,7 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
       float sum = 0.f;
       for (int i = (w - tiles) & 1; i < it.tiles; i += 2) {
         const uint32_t no = tiles + i, buf = no % kBufs;
-        ok = mbar_wait_inline(&s_full[buf], (no / kBufs) & 1, abort_flag);
+        ok = mbar_wait_spin(&s_full[buf], (no / kBufs) & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
         const uint32_t s_addr = tbase + lane_base + kTmemS + kRows * buf;
