@@ -26,11 +26,11 @@
  *    q8 layout: int8 [rows][128]. scales: float32 [G][rows] (group-major).
  *  - Every pointer is device memory owned by the caller; the library never
  *    allocates, frees or synchronises. Work is enqueued on `stream`, in stream
- *    order. The quantizers and the GEMM for M <= 64 are launched with
- *    programmatic stream serialization: their set-up may run while the
- *    previous kernel in the stream finishes. They read no input and write no
- *    output before that kernel has completed, so the ordering a caller sees is
- *    plain stream order.
+ *    order. The quantizers, the GEMM for M <= 64 and the paged cache's
+ *    operators but atom_kv4_evict are launched with programmatic stream
+ *    serialization: their set-up may run while the previous kernel in the
+ *    stream finishes. They read no input and write no output before that
+ *    kernel has completed, so the ordering a caller sees is plain stream order.
  *  - Errors a host check can see (null pointers, sizes, alignment, unsupported
  *    parameters) are returned before anything is launched. Errors only the
  *    device can see (a repeated or out-of-range outlier index, a bounded wait
@@ -423,11 +423,11 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *   cu_q         int32 [batch + 1]: rows cu_q[b] .. cu_q[b+1] - 1 of the call's
  *                row tensors are the new tokens of sequence b. Rows behind
  *                cu_q[batch] (padding) are neither read nor written.
- *   max_q        host bound on cu_q[b+1] - cu_q[b]; picks the kernels of
- *                atom_kv4_attention.
+ *   max_q        host bound on cu_q[b+1] - cu_q[b]: picks the kernels that read
+ *                queries. (A larger one costs time only.)
  * A sequence whose entries contradict the call (cu_q descending or above the
  * rows, more than max_q new tokens in atom_kv4_attention, kv_lens negative or
- * above max_pages * page_size) is skipped, a page outside [0, pages) is not
+ * above max_pages * page_size or 2^30) is skipped, a page outside [0, pages) is not
  * touched (attention reads its tokens as zeros), and either sets the device
  * status to ATOM_ERR_INVALID_ARG.
  *
@@ -467,8 +467,8 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *   token; NaN is smaller than everything). In their order they move to
  *   positions 0 .. new_len - 1 of `dst` (pages to_table int32
  *   [batch][to_table_stride], to_max_pages used). dst may be the source itself
- *   with the same pages: the eviction is then in place; otherwise no vector of
- *   dst may be one that is read. Written are
+ *   with the same pages, each of them one sequence's alone: the eviction is then
+ *   in place; otherwise no vector of dst may be one that is read. Written are
  *     new_lens     int32 [batch]: new_len; must not be batch->kv_lens.
  *     kept         int32 [batch][heads][budget]: the positions that stayed, then -1.
  *     new_weights  fp32 [batch][heads][new_width] or NULL: their weights (may be
@@ -476,9 +476,11 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *   cu_q and max_q are not read. budget >= 1, 0 <= recent <= budget,
  *   new_width >= budget.
  *
- * Every entry: rows, batch 0: no-op. Sizes above 2^31 - 1, a page_size < 1,
- * q_heads not a multiple of heads: ATOM_ERR_SHAPE. Inputs must be finite where
- * they are read; slots behind a sequence's last token may hold anything.
+ * Every entry: rows, batch 0: no-op. Sizes above 2^31 - 1, rows or query rows of
+ * a KV head above 2^30, a page_size < 1, q_heads not a multiple of heads:
+ * ATOM_ERR_SHAPE. Inputs must be finite where they are read; slots behind a
+ * sequence's last token may hold anything. Outputs share no memory with inputs
+ * or each other, but as said above. Stream-ordered, allocates nothing.
  */
 typedef struct atom_kv4_cache {
     uint8_t *k4;

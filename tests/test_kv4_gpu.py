@@ -419,3 +419,211 @@ def test_side_stream_and_captured_graph():
     a = atom.atom_kv4_attention(q, cache, batch, stream=other)
     other.synchronize()
     assert torch.equal(a[0], want[0])
+
+
+def test_a_captured_step_with_eviction():
+    """Append, attention, its weights and an eviction in place in one graph, replayed."""
+    c = Call(52, [1, 1], [200, 90], page=16, q_size=0.05, garbage=1.0)
+    cache, lens = c.device_cache(), dev(c.lens)
+    batch = atom.KV4Batch(dev(c.table), lens, dev(c.cu_q), max_q=1)
+    q, k, v = dev(c.q), dev(c.k), dev(c.v)
+    first = [t.clone() for t in (cache.k4, cache.ks, cache.v4, cache.vs)]
+    sums = torch.zeros((2, 2, 256), device="cuda")
+    new_lens = torch.empty(2, dtype=torch.int32, device="cuda")
+
+    def step():
+        atom.atom_kv4_append(k, v, cache, batch)
+        out, lse = atom.atom_kv4_attention(q, cache, batch)
+        atom.atom_kv4_attention_weights(q, lse, cache, batch, sums, prev=sums)
+        kept, _ = atom.atom_kv4_evict(sums, cache, batch, 100, 20, cache, batch.block_table,
+                                      new_lens, new_weights=sums)
+        return out, lse, kept
+
+    def restart():
+        for t, f in zip((cache.k4, cache.ks, cache.v4, cache.vs), first):
+            t.copy_(f)
+        sums.zero_()
+        lens.copy_(dev(c.lens))
+
+    def state(outs):
+        return [t.clone() for t in (*outs, cache.k4, cache.ks, cache.v4, cache.vs, sums, new_lens)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    runs = []
+    for run in (step, lambda: graph.replay() or outs):
+        restart()
+        one = state(run())
+        lens.copy_(new_lens)           # the next step's token is the last that stayed
+        runs.append(one + state(run()))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    assert host(new_lens).tolist() == [100, 90]
+
+
+def test_weights_of_a_sequence_without_new_tokens():
+    """`max_q` is a bound: one sequence may have none, and its sums are still written."""
+    c = Call(59, [0], [300], page=16, q_size=0.05, pad_rows=3)
+    lse = torch.zeros((3, 8), device="cuda")
+    prev = torch.rand((1, 2, 310), device="cuda")
+    sums = torch.full_like(prev, 7.0)
+    atom.atom_kv4_attention_weights(dev(c.q), lse, c.device_cache(), c.device_batch(max_q=100), sums,
+                                    prev=prev)
+    assert torch.equal(sums[..., :300], prev[..., :300]) and bool((sums[..., 300:] == 7).all())
+
+
+def test_two_streams_at_once():
+    """The same work on two streams at a time, each call with its own workspace."""
+    cases = [Call(60, [1] * 5, [700, 3, 2000, 64, 900], page=16, q_size=0.05),
+             Call(61, [130] * 10, [300] * 10, q_heads=8, heads=8, page=16, q_size=0.05)]
+    work = [(dev(c.q), c.device_cache(), c.device_batch(),
+             torch.zeros((len(c.lens), c.heads, 2000), device="cuda")) for c in cases]
+
+    def run(q, cache, batch, sums, stream):
+        out, lse = atom.atom_kv4_attention(q, cache, batch, stream=stream)
+        atom.atom_kv4_attention_weights(q, lse, cache, batch, sums, stream=stream)
+        return out, lse, sums
+
+    want = [[t.clone() for t in run(*w, None)] for w in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(20):
+        got = [run(*w, s) for w, s in zip(work, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_a_sequence_listed_twice():
+    """Sequences that share their pages (a common prefix) read the same tokens."""
+    c = Call(62, [2, 2], [300, 300], page=16, q_size=0.05)
+    c.table[1] = c.table[0]
+    c.q[2:4] = c.q[:2]
+    out, lse = check_attention(c)
+    assert torch.equal(out[:2], out[2:]) and torch.equal(lse[:2], lse[2:])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+@pytest.mark.parametrize("new,heads", [([1, 3], 2), ([150] * 10, 5)])
+def test_scales_of_zero_and_below(scale, new, heads):
+    check_attention(Call(63, new, [200 + i for i in range(len(new))], q_heads=2 * heads, heads=heads,
+                         page=16, q_size=0.05), scale=scale)
+
+
+def test_pool_beyond_32_bits():
+    """Codes at byte offsets beyond 2^32: the last pages of a pool of 4.6 GB."""
+    pages, size, heads = 140_000, 64, 8
+    c = Call(64, [3, 70], [150, 200], q_heads=16, heads=heads, page=size, q_size=0.05)
+    free, _ = torch.cuda.mem_get_info()
+    if free < 12 * 2 ** 30:
+        pytest.skip("needs 12 GB")
+    base = pages - 1 - int(c.table.max())
+    big = [torch.empty((pages, size, heads, n), dtype=t, device="cuda").squeeze(-1) if n == 1 else
+           torch.empty((pages, size, heads, n), dtype=t, device="cuda")
+           for n, t in ((64, torch.uint8), (1, torch.float32)) * 2]
+    for t, a in zip(big, c.cache):
+        t[base:base + a.shape[0]].copy_(torch.from_numpy(np.ascontiguousarray(a)).cuda())
+    cache = atom.KV4Cache(*big)
+    table = np.where(c.table >= 0, c.table + base, -1).astype(np.int32)
+    batch = atom.KV4Batch(dev(table), dev(c.lens), dev(c.cu_q), max_q=70)
+    want = [a.copy() for a in c.cache]
+    atom.atom_kv4_append(dev(c.k), dev(c.v), cache, batch)
+    ko.append(c.k, c.v, want, *c.sequences())
+    for t, a in zip(big, want):
+        assert np.array_equal(host(t[base:base + a.shape[0]]), a, equal_nan=a.dtype == np.float32)
+    out, lse = atom.atom_kv4_attention(dev(c.q), cache, batch)
+    ref = ko.attention(c.q, want, *c.sequences(), True, SCALE)
+    assert_within(host(out), ref[0], ref[1], "out")
+    assert_within(host(lse), ref[2], ref[3], "lse")
+    sums = torch.zeros((2, heads, 200), device="cuda")
+    atom.atom_kv4_attention_weights(dev(c.q), lse, cache, batch, sums)
+    s, tol = ko.attention_weights(c.q, host(lse), want, *c.sequences(), True, SCALE, 200)
+    inside = np.broadcast_to(np.arange(200)[None, None] < c.lens[:, None, None], s.shape)
+    assert_within(host(sums)[inside], s[inside], tol[inside], "sums")
+    new_lens = torch.empty(2, dtype=torch.int32, device="cuda")
+    kept, _ = atom.atom_kv4_evict(sums, cache, batch, 100, 10, cache, batch.block_table, new_lens)
+    at = host(kept)
+    for b in range(2):
+        for h in range(heads):
+            i, j = at[b, h], np.arange(100)
+            src, dst = (c.table[b, i // size], i % size, h), (c.table[b, j // size], j % size, h)
+            for t, a in zip(big, want):
+                assert np.array_equal(host(t[base:base + a.shape[0]])[dst], a[src])
+
+
+def test_arrays_that_contradict_the_call():
+    """What only the device can see: the sequence is skipped or the page's tokens are zeros, the
+    others are as ever, and the status says so."""
+    good = Call(65, [2, 2, 2, 2], [40, 50, 60, 70], page=16, q_size=0.05, garbage=1.0)
+    want = ko.attention(good.q, good.cache, *good.sequences(), True, SCALE)
+    lens, table, cu_q = good.lens.copy(), good.table.copy(), good.cu_q.copy()
+    lens[1] = 16 * table.shape[1] + 1          # more than the table has
+    lens[2] = -3
+    cache = good.device_cache()
+    batch = atom.KV4Batch(dev(table), dev(lens), dev(cu_q), max_q=2)
+    out = torch.full((8, 8, 128), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((8, 8), 7.0, device="cuda")
+    sums = torch.full((4, 2, 80), 7.0, device="cuda")
+    before = [t.clone() for t in (cache.k4, cache.ks, cache.v4, cache.vs)]
+
+    def status():
+        return atom.atom_device_status(clear=True)
+
+    atom.atom_kv4_attention(dev(good.q), cache, batch, out=out, lse=lse)
+    assert status() == 1
+    for rows in (slice(0, 2), slice(6, 8)):
+        assert_within(host(out)[rows], want[0][rows], want[1][rows], "out")
+    assert bool((out[2:6] == 7).all()) and bool((lse[2:6] == 7).all())
+    atom.atom_kv4_attention_weights(dev(good.q), lse, cache, batch, sums)
+    assert status() == 1
+    assert bool((sums[1:3] == 7).all()) and not bool((sums[0, :, :40] == 7).any())
+    atom.atom_kv4_append(dev(good.k), dev(good.v), cache, batch)
+    assert status() == 1
+    ref = [a.copy() for a in good.cache]
+    keep = (table[[0, 3]], lens[[0, 3]], np.array([0, 2, 4], np.int32))
+    ko.append(good.k[[0, 1, 6, 7]], good.v[[0, 1, 6, 7]], ref, *keep)
+    for t, a, b in zip((cache.k4, cache.ks, cache.v4, cache.vs), ref, before):
+        assert np.array_equal(host(t), a)
+        t.copy_(b)
+    new_lens = torch.full((4,), 7, dtype=torch.int32, device="cuda")
+    atom.atom_kv4_evict(sums, cache, batch, 30, 5, cache, batch.block_table, new_lens)
+    assert status() == 1 and host(new_lens).tolist() == [30, 7, 7, 30]
+    # too many new tokens, descending starts
+    small = atom.KV4Batch(dev(table), dev(good.lens), dev(cu_q), max_q=1)
+    atom.atom_kv4_attention(dev(good.q), cache, small, out=out.fill_(7))
+    assert status() == 1 and bool((out == 7).all())
+    cu_q[2] = 1
+    atom.atom_kv4_attention(dev(good.q), cache, atom.KV4Batch(dev(table), dev(good.lens), dev(cu_q),
+                                                             max_q=8), out=out)
+    assert status() == 1
+
+
+@pytest.mark.parametrize("new", [1, 20, 130])
+@pytest.mark.parametrize("page", [16, 64])
+def test_pages_outside_the_pool_read_as_zeros(new, page):
+    c = Call(66, [new] * 16, [200] * 16, q_heads=4, heads=4, page=page, q_size=0.05, garbage=1.0)
+    cache = c.device_cache()
+    bad = c.table.copy()
+    bad[3, 1], bad[5, 0], bad[5, 2] = len(c.cache[0]), -1, 2 ** 31 - 1
+    batch = atom.KV4Batch(dev(bad), dev(c.lens), dev(c.cu_q), max_q=new)
+    # the oracle reads zeros in pages of their own
+    arrays = [np.concatenate([a, np.zeros((1, *a.shape[1:]), a.dtype)]) for a in c.cache]
+    table = np.where((bad < 0) & (np.arange(bad.shape[1]) * page < 200) | (bad >= len(c.cache[0])),
+                     len(c.cache[0]), bad)
+    out, lse = atom.atom_kv4_attention(dev(c.q), cache, batch)
+    assert atom.atom_device_status(clear=True) == 1
+    want = ko.attention(c.q, arrays, table, c.lens, c.cu_q, True, SCALE)
+    assert_within(host(out), want[0], want[1], "out")
+    assert_within(host(lse), want[2], want[3], "lse")
+    sums = torch.zeros((16, 4, 200), device="cuda")
+    atom.atom_kv4_attention_weights(dev(c.q), lse, cache, batch, sums)
+    assert atom.atom_device_status(clear=True) == 1
+    s, tol = ko.attention_weights(c.q, host(lse), arrays, table, c.lens, c.cu_q, True, SCALE, 200)
+    assert_within(host(sums), s, tol, "sums")

@@ -34,6 +34,8 @@ int limit(int qn, int len, int qi, int causal) {
 }
 uint32_t weight_key(uint32_t bits) { return kv4_weight_key(bits); }
 int64_t part_begin(int64_t total, int parts, int i) { return kv4_part_begin(total, parts, i); }
+int capacity(int64_t max_pages, int64_t page_size) { return kv4_capacity(max_pages, page_size); }
+int64_t few_rows(int64_t pairs, int64_t max_rows, int sms) { return kv4_few_rows(pairs, max_rows, sms); }
 
 // The decode kernel's division of a call among `ctas` CTAs, walked through on
 // the host. Counts how often every (tile, unit) is computed, checks that a
@@ -133,6 +135,24 @@ def test_limits(plan):
     assert [plan.limit(3, 10, i, 0) for i in range(3)] == [10, 10, 10]
     assert [plan.limit(4, 2, i, 1) for i in range(4)] == [0, 0, 1, 2]
     assert plan.limit(2 ** 31 - 1, 0, 0, 1) == 0
+
+
+def test_positions_stay_below_2_to_30(plan):
+    plan.capacity.argtypes = [ct.c_int64, ct.c_int64]
+    for pages, size, want in [(0, 16, 0), (0, 2 ** 31 - 1, 0), (3, 16, 48), (2 ** 30, 1, 2 ** 30),
+                              (2 ** 30 + 1, 1, 2 ** 30), (1, 2 ** 31 - 1, 2 ** 30),
+                              (2 ** 26, 16, 2 ** 30), (2 ** 62, 3, 2 ** 30)]:
+        assert plan.capacity(pages, size) == want
+
+
+def test_rows_that_the_decode_kernel_takes(plan):
+    plan.few_rows.argtypes = [ct.c_int64, ct.c_int64, ct.c_int]
+    plan.few_rows.restype = ct.c_int64
+    for pairs in [1, 2, 7, 36, 64, 128, 148, 149, 300, 512, 10 ** 4, 2 ** 31, 2 ** 62]:
+        rows = [plan.few_rows(pairs, m, 148) for m in (1, 16, 17, 300, 10 ** 5, 2 ** 30)]
+        assert rows[0] == rows[1] == 16 and rows == sorted(rows) and rows[-1] <= 4096
+        assert all(r % 16 == 0 for r in rows)
+    assert plan.few_rows(8, 10 ** 6, 148) > plan.few_rows(128, 10 ** 6, 148) >= 48
 
 
 def test_weight_keys_order_as_the_weights(plan):
@@ -288,6 +308,13 @@ def test_eviction_is_checked_on_the_host(lib, kw, expect):
 
 def q4(*lead):
     return torch.zeros(*lead, 64, dtype=torch.uint8)
+
+
+def test_more_rows_than_2_to_30_are_refused(lib):
+    assert append(lib, rows=2 ** 30 + 1) == SHAPE
+    assert attention(lib, rows=2 ** 30 + 1, q_heads=2) == SHAPE
+    assert attention(lib, rows=2 ** 28 + 1, q_heads=8) == SHAPE
+    assert weights(lib, rows=2 ** 29 + 1, q_heads=4) == SHAPE
 
 
 def test_binding_checks_a_cache():

@@ -5,6 +5,8 @@
 namespace {
 
 bool kv4_fits(int64_t v) { return v <= INT32_MAX; }
+// Rows leave room for the loops that step past them in 32 bits.
+bool kv4_fits_rows(int64_t v) { return v <= atomk::kKv4MaxPositions; }
 
 // Sizes and strides, then (with `touched`) pointers.
 atom_status_t kv4_check_cache(const atom_kv4_cache_t *c, bool touched) {
@@ -82,10 +84,6 @@ atomk::Kv4Geom kv4_geom(const atom_kv4_cache_t *c) {
   return g;
 }
 
-int kv4_capacity(int64_t max_pages, int64_t page_size) {
-  return max_pages > INT32_MAX / page_size ? INT32_MAX : static_cast<int>(max_pages * page_size);
-}
-
 atomk::Kv4Seqs kv4_seqs(const atom_kv4_batch_t *b, const atom_kv4_cache_t *c, int64_t rows) {
   atomk::Kv4Seqs s;
   s.table = b->block_table;
@@ -94,7 +92,7 @@ atomk::Kv4Seqs kv4_seqs(const atom_kv4_batch_t *b, const atom_kv4_cache_t *c, in
   s.cu_q = b->cu_q;
   s.batch = static_cast<int>(b->batch);
   s.rows = static_cast<int>(rows);
-  s.capacity = kv4_capacity(b->max_pages, c->page_size);
+  s.capacity = atomk::kv4_capacity(b->max_pages, c->page_size);
   return s;
 }
 
@@ -120,7 +118,7 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
                        int64_t v_token, int64_t v_head, int64_t rows, const atom_kv4_cache_t *cache,
                        const atom_kv4_batch_t *batch, atom_stream_t stream) {
   if (rows < 0) return ATOM_ERR_INVALID_ARG;
-  if (!kv4_fits(rows)) return ATOM_ERR_SHAPE;
+  if (!kv4_fits_rows(rows)) return ATOM_ERR_SHAPE;
   const bool touched = rows > 0 && batch != nullptr && batch->batch > 0;
   atom_status_t st;
   if ((st = kv4_check_cache(cache, touched)) != ATOM_OK) return st;
@@ -157,24 +155,8 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
   return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 
-// Largest number of query rows of a KV head that goes to the decode kernel where
-// a call has `pairs` (sequence, KV head) pairs with up to `max_rows` of them; more
-// go to the prompt kernel.
-// The decode kernel reads the cache once per 16 rows and divides that evenly over
-// the GPU: 44 us per million tokens, pair and 16 rows. The prompt kernel reads it
-// once per 256 rows, with one CTA an SM and a CTA a pair and 256 rows: 22 us per
-// thousand tokens for each round of CTAs. (Both measured: 16 sequences of 3000
-// tokens, 8 heads, 64 rows 76 and 77 us, 128 rows 139 and 78; one sequence, 512
-// rows 44 and 73.)
-int64_t kv4_few_rows(int64_t pairs, int64_t max_rows, int sms) {
-  int64_t rows = 16;
-  for (; rows < max_rows && rows < 4096; rows += 16) {
-    const int64_t rounds = (pairs * ((rows + 16 + 255) / 256) + sms - 1) / sms;
-    if (pairs * ((rows + 16) / 16) >= 500 * rounds) break;
-  }
-  return rows;
-}
-// The same for the attention weights: 64 sequences of 8192 tokens with 8 rows 77
+// Largest number of query rows of a KV head that goes to the first kernel of the
+// attention weights (kv4_few_rows is the attention's): 64 sequences of 8192 tokens with 8 rows 77
 // us in the first kernel; 16 of 3000, 8 heads, 24 rows 43 and 45, 32 rows 54 and 45.
 constexpr int kKv4WeightFewRows = 24;
 
@@ -243,8 +225,8 @@ atom_status_t kv4_check_queries(int64_t rows, int64_t q_heads, float scale,
   atom_status_t st;
   if ((st = kv4_check_cache(cache, *touched)) != ATOM_OK) return st;
   if ((st = kv4_check_batch(batch, *touched)) != ATOM_OK) return st;
-  if (!kv4_fits(rows) || q_heads < 1 || q_heads % cache->heads != 0 || !kv4_fits(q_heads) ||
-      !kv4_fits(rows * (q_heads / cache->heads)))   // query rows of a KV head
+  if (!kv4_fits_rows(rows) || q_heads < 1 || q_heads % cache->heads != 0 || !kv4_fits(q_heads) ||
+      !kv4_fits_rows(rows * (q_heads / cache->heads)))   // query rows of a KV head
     return ATOM_ERR_SHAPE;
   return ATOM_OK;
 }
@@ -315,7 +297,7 @@ atom_status_t atom_kv4_attention(const void *q, int64_t q_token, int64_t q_head,
   // Sequences with few query rows a KV head go to the decode kernel, those with
   // more to the prompt kernel; one that no sequence can need is not launched.
   CUtensorMap q_map;
-  const int64_t few_rows = kv4_few_rows(batch->batch * cache->heads,
+  const int64_t few_rows = atomk::kv4_few_rows(batch->batch * cache->heads,
                                         static_cast<int64_t>(p.max_q) * p.group, dev->sm_count);
   const bool prompts =
       kv4_prompt_call(&q_map, q, q_token, q_head, rows, q_heads, p.group, p.max_q, few_rows);
@@ -394,7 +376,8 @@ atom_status_t atom_kv4_attention_weights(const void *q, int64_t q_token, int64_t
                                        kKv4WeightFewRows);
   const bool few = !prompts || batch->batch > 1;
   p.tile_rows = prompts ? 128 / p.group * p.group : 0;
-  p.few_rows = !prompts ? INT32_MAX : (few ? kKv4WeightFewRows : 0);
+  // (alone, the second kernel also takes a sequence without new tokens)
+  p.few_rows = !prompts ? INT32_MAX : (few ? kKv4WeightFewRows : -1);
   cudaError_t err = cudaSuccess;
   if (prompts) {
     using namespace atomk::kv4_wprompt_cfg;
@@ -455,7 +438,7 @@ atom_status_t atom_kv4_evict(const float *weights, int64_t width, const atom_kv4
   p.to_geom = kv4_geom(dst);
   p.to_table = to_table;
   p.to_table_stride = to_table_stride;
-  p.to_capacity = kv4_capacity(to_max_pages, dst->page_size);
+  p.to_capacity = atomk::kv4_capacity(to_max_pages, dst->page_size);
   p.budget = static_cast<int>(budget);
   p.recent = static_cast<int>(recent);
   p.new_lens = new_lens;

@@ -40,8 +40,15 @@ struct Kv4Geom {
   Kv4Div by_page;
 };
 
-// The sequences of a call. Positions are 32-bit: `capacity` is the smaller of
-// max_pages * page_size and 2^31 - 1.
+// Positions and rows are 32-bit, and stay so far below 2^31 that loops may step
+// past them.
+constexpr int kKv4MaxPositions = 1 << 30;
+inline int kv4_capacity(int64_t max_pages, int64_t page_size) {
+  return max_pages > kKv4MaxPositions / page_size ? kKv4MaxPositions
+                                                  : static_cast<int>(max_pages * page_size);
+}
+
+// The sequences of a call; `capacity` is what kv4_capacity says.
 struct Kv4Seqs {
   const int32_t *table;    // [batch][table_stride], pages of each sequence
   int64_t table_stride;
@@ -113,6 +120,24 @@ KV4_HD int kv4_part_of(int64_t total, int parts, int64_t at) {
   return static_cast<int>(((at + 1) * parts - 1) / total);
 }
 
+// Largest number of query rows of a KV head that goes to the decode kernel where
+// a call has `pairs` (sequence, KV head) pairs with up to `max_rows` of them; more
+// go to the prompt kernel.
+// The decode kernel reads the cache once per 16 rows and divides that evenly over
+// the GPU: 44 us per million tokens, pair and 16 rows. The prompt kernel reads it
+// once per 256 rows, with one CTA an SM and a CTA a pair and 256 rows: 22 us per
+// thousand tokens for each round of CTAs. (Both measured: 16 sequences of 3000
+// tokens, 8 heads, 64 rows 76 and 77 us, 128 rows 139 and 78; one sequence, 512
+// rows 44 and 73.)
+inline int64_t kv4_few_rows(int64_t pairs, int64_t max_rows, int sms) {
+  if (pairs > int64_t(1) << 40) pairs = int64_t(1) << 40;   // (the products stay in 64 bits)
+  int64_t rows = 16;
+  for (; rows < max_rows && rows < 4096; rows += 16) {
+    const int64_t rounds = (pairs * ((rows + 16 + 255) / 256) + sms - 1) / sms;
+    if (pairs * ((rows + 16) / 16) >= 500 * rounds) break;
+  }
+  return rows;
+}
 // Sort key of an accumulated weight: larger weights have larger keys, the two
 // zeros the same, NaN the smallest.
 KV4_HD uint32_t kv4_weight_key(uint32_t bits) {

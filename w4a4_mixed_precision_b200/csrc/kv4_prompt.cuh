@@ -383,15 +383,17 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
   // rows of the query tiles that no copy reaches
   for (uint32_t i = threadIdx.x; i < 2 * kQTile / 16; i += kThreads)
     st_shared_v4(smem + kQOff + 16 * i, 0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   grid_dependency_wait();
+  // (not before: a CTA of the kernel before this one, on the same SM, may still be
+  // about to allocate, and would wait for a CTA that waits for it)
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
   const Kv4Line line = kv4_find_place<kThreads / 32>(
       p.seqs, [&](const Kv4Seq &s) { return kv4_prompt_weight(s, p); },
       [](const Kv4Seq &) { return 0; },

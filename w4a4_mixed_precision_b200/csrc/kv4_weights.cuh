@@ -414,15 +414,17 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
   // rows of the query tiles that no copy reaches
   for (uint32_t i = threadIdx.x; i < kStages * kTile / 16; i += kThreads)
     st_shared_v4(smem + kQOff + 16 * i, 0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   grid_dependency_wait();
+  // (not before: a CTA of the kernel before this one, on the same SM, may still be
+  // about to allocate, and would wait for a CTA that waits for it)
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
   const Kv4Line line = kv4_find_place<kThreads / 32>(
       p.seqs, [&](const Kv4Seq &s) { return kv4_wprompt_weight(s, p); },
       [](const Kv4Seq &) { return 0; },
@@ -638,6 +640,7 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
       Kv4WItem it;
       if (!(ok = take_item(it)) || !it.more) break;
       ok = mbar_wait(&k_full[items & 1], (items >> 1) & 1, abort_flag);
+      if (it.tiles == 0 && leader) tc_commit(&k_empty[items & 1]);   // no new tokens
       for (int i = 0; ok && i < it.tiles; ++i, ++tiles) {
         const uint32_t st = tiles % kStages, buf = tiles % kBufs;
         ok = mbar_wait(&s_empty[buf], ((tiles / kBufs) & 1) ^ 1u, abort_flag) &&
