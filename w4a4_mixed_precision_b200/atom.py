@@ -13,6 +13,7 @@ Layouts (see include/atom.h): for R rows of K channels with G = K/128,
 from __future__ import annotations
 
 import ctypes as ct
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -557,8 +558,11 @@ def _kv4_contiguous(t: torch.Tensor, dtype: torch.dtype, shape, name: str, devic
 def _kv4_output(t: Optional[torch.Tensor], like: torch.Tensor, dtype: torch.dtype, shape, name: str,
                 device) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one on `like`'s device."""
-    if t is None:   # (naming a type costs some microseconds)
-        return like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
+    if t is None:   # (naming a shape, then a type, costs from half a microsecond to some)
+        if like.dtype != dtype:
+            return like.new_empty(shape, dtype=dtype)
+        same = like.is_contiguous() and like.shape == shape
+        return torch.empty_like(like) if same else like.new_empty(shape)
     _kv4_contiguous(t, dtype, shape, name, device)
     return t
 
@@ -703,6 +707,11 @@ def atom_kv4_attention_workspace_bytes(rows: int, q_heads: int, heads: int, max_
     return int(lib().atom_kv4_attention_workspace_bytes(rows, q_heads, heads, max_q))
 
 
+@functools.lru_cache(maxsize=64)
+def _kv4_workspace_bytes(device_index: int, *sizes: int) -> int:
+    return atom_kv4_attention_workspace_bytes(*sizes)   # of the current device, device_index
+
+
 def atom_kv4_attention(q: torch.Tensor, cache: KV4Cache, batch: KV4Batch, causal: bool = True,
                        scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                        lse: Optional[torch.Tensor] = None,
@@ -729,8 +738,8 @@ def atom_kv4_attention(q: torch.Tensor, cache: KV4Cache, batch: KV4Batch, causal
         ws, ws_bytes = workspace, 0
         if split:
             if ws is None:
-                ws_bytes = lib().atom_kv4_attention_workspace_bytes(rows, q_heads, cache.heads,
-                                                                    batch.max_q)
+                ws_bytes = _kv4_workspace_bytes(device.index, rows, q_heads, cache.heads,
+                                                batch.max_q)
                 ws = cache.k4.new_empty(ws_bytes) if ws_bytes else None
             else:
                 ws_bytes = ws.numel()

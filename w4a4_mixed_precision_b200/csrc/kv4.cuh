@@ -88,8 +88,9 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_kernel(const Kv4Rows p) {
           b[u] = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
         } else {
           const int64_t vec = vec0 + static_cast<int64_t>(head) * p.geom.head_stride;
-          const uint2 q = __ldg(reinterpret_cast<const uint2 *>((value ? p.v4 : p.k4) + vec * 64 + sub * 8));
-          a[u] = make_uint4(q.x, q.y, __float_as_uint(__ldg((value ? p.vs : p.ks) + vec)), 0u);
+          // words `sub` and 8 + `sub`, so that a team writes 128 bytes in one piece
+          const uint32_t *q = reinterpret_cast<const uint32_t *>((value ? p.v4 : p.k4) + vec * 64) + sub;
+          a[u] = make_uint4(__ldg(q), __ldg(q + 8), __float_as_uint(__ldg((value ? p.vs : p.ks) + vec)), 0u);
         }
       }
 #pragma unroll
@@ -110,9 +111,9 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_kernel(const Kv4Rows p) {
           kv_decode16(make_uint2(a[u].x, a[u].y), __uint_as_float(a[u].z), o);
           uint4 *dst = reinterpret_cast<uint4 *>(
               (value ? p.v + row * p.v_token + head * p.v_head
-                     : p.k + row * p.k_token + head * p.k_head) + sub * 16);
+                     : p.k + row * p.k_token + head * p.k_head) + sub * 8);
           dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          dst[8] = make_uint4(o[4], o[5], o[6], o[7]);
         }
       }
     }
