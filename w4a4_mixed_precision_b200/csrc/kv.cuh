@@ -96,10 +96,10 @@ __device__ __forceinline__ void kv_decode16(uint2 p, float s, uint32_t (&o)[8]) 
     // (= 1.5*2^23 + (n ^ 8)) minus 1.5*2^23 + 8, both steps exact. The pair
     // of products goes to fp16 in one packed round-to-nearest conversion.
     const uint32_t byte = w[j >> 2] >> (8 * (j & 3));
-    const float q0 = __fsub_rn(__uint_as_float(0x4B400000u | ((byte & 0xFu) ^ 8u)), 12582920.f);
-    const float q1 =
-        __fsub_rn(__uint_as_float(0x4B400000u | (((byte >> 4) & 0xFu) ^ 8u)), 12582920.f);
-    o[j] = pack_half2_rn(__fmul_rn(q0, s), __fmul_rn(q1, s));
+    const float2 biased = make_float2(__uint_as_float((byte & 0xFu) ^ 0x4B400008u),
+                                      __uint_as_float(((byte >> 4) & 0xFu) ^ 0x4B400008u));
+    const float2 v = f2_mul(f2_add(biased, make_float2(-12582920.f, -12582920.f)), make_float2(s, s));
+    o[j] = pack_half2_rn(v.x, v.y);
   }
 }
 
