@@ -311,6 +311,14 @@ def test_evict_matches_the_oracle(lens, budget, recent, page, to_page, token_maj
                 host(new_w))
 
 
+@pytest.mark.parametrize("budget,recent", [(1, 0), (100, 30), (257, 257), (600, 64)])
+def test_evict_many_sequences(budget, recent):
+    """More (sequence, head)s than the GPU holds of the larger CTAs at once."""
+    rng = np.random.default_rng(11)
+    lens = np.concatenate([[0, 1, 2, 3000], rng.integers(0, 700, 200)])
+    test_evict_matches_the_oracle(lens.tolist(), budget, recent, 16, 16, False)
+
+
 def check_moved(c, w, kept, lens, got, table, page, new_w):
     got = [host(x) for x in got]
     for b, n in enumerate(lens):

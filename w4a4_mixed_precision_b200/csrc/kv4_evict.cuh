@@ -54,7 +54,7 @@ struct Kv4Evict {
 
 namespace kv4_evict_cfg {
 constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kFewThreads = 256;         // where there are many (sequence, head)s
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kRun = 8;                  // tokens a thread numbers at once
@@ -75,9 +75,13 @@ __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t cluster_addr) {
   return v;
 }
 
-__global__ void __launch_bounds__(kv4_evict_cfg::kThreads, 2)
-kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
+// T threads; with kFewThreads no cluster.
+template <int T>
+__global__ void __launch_bounds__(T, 1024 / T)
+kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster_size) {
   using namespace kv4_evict_cfg;
+  constexpr int kWarps = T / 32, kOwnBins = kBins / T;
+  const int cluster = T == kThreads ? cluster_size : 1;
   extern __shared__ __align__(16) uint8_t kv4_smem[];
   uint32_t *keys = reinterpret_cast<uint32_t *>(kv4_smem);
   __shared__ __align__(16) int hist[kBins];
@@ -118,16 +122,16 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
   // flight together.
   const bool in_smem = old_hi - lo <= p.keys;
   if (in_smem && want > 0 && want < old) {
-    for (int i0 = lo; i0 < old_hi; i0 += 8 * kThreads) {
+    for (int i0 = lo; i0 < old_hi; i0 += 8 * T) {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * kThreads + tid;
+        const int i = i0 + j * T + tid;
         v[j] = i < old_hi ? w[i] : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * kThreads + tid;
+        const int i = i0 + j * T + tid;
         if (i < old_hi) keys[i - lo] = kv4_weight_key(__float_as_uint(v[j]));
       }
     }
@@ -152,10 +156,10 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
       const uint32_t bins = pass == 2 ? 1023u : 2047u;
       const uint32_t mask = pass == 0 ? 0u : (pass == 1 ? 0xFFE00000u : 0xFFFFFC00u);
-      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+      for (int i = tid; i < kBins; i += T) hist[i] = 0;
       __syncthreads();
 #pragma unroll 8
-      for (int i0 = lo; i0 < old_hi; i0 += kThreads) {
+      for (int i0 = lo; i0 < old_hi; i0 += T) {
         const int i = i0 + tid;
         const uint32_t key = i < old_hi ? key_of(i) : 0u;
         const bool is = i < old_hi && (key & mask) == known;
@@ -163,15 +167,22 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       }
       sync_all();
       // the bin at which the count from above reaches `need`; thread t has the
-      // bins kBins - 1 - 4t .. - 3
-      const int4 here = *reinterpret_cast<const int4 *>(&hist[kBins - 4 - 4 * tid]);
-      int mine[4] = {here.w, here.z, here.y, here.x}, own = 0;
-      if (cluster > 1) {
+      // kOwnBins below kBins - kOwnBins * t
+      const int top_bin = kBins - 1 - kOwnBins * tid;
+      int mine[kOwnBins], own = 0;
+#pragma unroll
+      for (int j = 0; j < kOwnBins; j += 4) {
+        const int4 here = *reinterpret_cast<const int4 *>(&hist[top_bin - 3 - j]);
+        mine[j] = here.w;
+        mine[j + 1] = here.z;
+        mine[j + 2] = here.y;
+        mine[j + 3] = here.x;
+      }
+      if (cluster > 1) {   // (kOwnBins is 4)
         int4 v[kMaxCluster - 1];
 #pragma unroll
         for (int c = 1; c < kMaxCluster; ++c)
-          v[c - 1] = c < cluster ? ld_shared_cluster_v4s(cluster_map(&hist[kBins - 4 - 4 * tid],
-                                                                     (rank + c) % cluster))
+          v[c - 1] = c < cluster ? ld_shared_cluster_v4s(cluster_map(&hist[top_bin - 3], (rank + c) % cluster))
                                  : make_int4(0, 0, 0, 0);
 #pragma unroll
         for (int c = 1; c < kMaxCluster; ++c) {
@@ -181,7 +192,9 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
           mine[3] += v[c - 1].x;
         }
       }
-      const int total = mine[0] + mine[1] + mine[2] + mine[3];
+      int total = 0;
+#pragma unroll
+      for (int j = 0; j < kOwnBins; ++j) total += mine[j];
       int upto = total;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -194,9 +207,9 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       int above = upto - total;
       if (above < need && upto >= need) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kOwnBins; ++j) {
           if (above < need && above + mine[j] >= need) {
-            found_bin = kBins - 1 - 4 * tid - j;
+            found_bin = top_bin - j;
             found_above = above;
           }
           above += mine[j];
@@ -208,8 +221,8 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       need -= found_above;
       // this CTA's own tokens above it
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (kBins - 1 - 4 * tid - j > bin) own += hist[kBins - 1 - 4 * tid - j];
+      for (int j = 0; j < kOwnBins; ++j)
+        if (top_bin - j > bin) own += hist[top_bin - j];
       own = __reduce_add_sync(0xffffffffu, own);
       if (lane == 0) scan[1][warp] = own;
       __syncthreads();
@@ -237,7 +250,7 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
     }
   }
 #pragma unroll 1
-  for (int base = lo; base < old_hi; base += kThreads * kRun) {
+  for (int base = lo; base < old_hi; base += T * kRun) {
     const int i0 = base + tid * kRun;
     unsigned above = 0, equal = 0;   // bits: tokens i0 ..
     uint32_t run[kRun];
@@ -289,8 +302,8 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
       e += is_equal;
     }
   }
-  for (int i = old + rank * kThreads + tid; i < len; i += cluster * kThreads) kept[want + i - old] = i;
-  for (int i = new_len + rank * kThreads + tid; i < p.budget; i += cluster * kThreads) kept[i] = -1;
+  for (int i = old + rank * T + tid; i < len; i += cluster * T) kept[want + i - old] = i;
+  for (int i = new_len + rank * T + tid; i < p.budget; i += cluster * T) kept[i] = -1;
   sync_all();
 
   // ---- move them. A warp takes 32 tokens at a time: a lane finds the addresses
@@ -314,7 +327,7 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster) {
     to_page = __ldg(to_table + to_page_no);
   };
   // steps: as many warps as the cluster has, 32 tokens each
-  const int step = cluster * kThreads;
+  const int step = cluster * T;
   const int first = (rank * kWarps + warp) * 32 + lane;
   look_up(first);
   for (int base = 0; base < new_len; base += step) {
