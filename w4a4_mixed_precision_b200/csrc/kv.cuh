@@ -52,7 +52,8 @@ __device__ __forceinline__ uint2 kv_encode16(const uint32_t (&w)[8], unsigned te
   }
   // the low byte of fp32(1.5 * 2^23 + rint(x * inv)) is the code in two's
   // complement; the product is rounded to fp32 before the add rounds to an
-  // integer (__fmul_rn / __fadd_rn are never contracted into an FMA)
+  // integer (__fmul_rn / __fadd_rn are never contracted into an FMA; packed
+  // products and sums were)
   uint32_t c[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) c[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[j], inv), 12582912.f));

@@ -59,11 +59,13 @@ __device__ __forceinline__ int64_t kv4_row_vector(const Kv4Rows &p, int row) {
 
 constexpr int kKv4RowVecs = 16;   // of a row, per warp
 
+// (At least 3 and 5 CTAs an SM: 80 registers instead of 100 for append's, 9 x 4000
+// tokens 62 -> 58 us with the gather.)
 template <bool kAppend>
-__global__ void __launch_bounds__(kKvThreads) kv4_rows_kernel(const Kv4Rows p) {
+__global__ void __launch_bounds__(kKvThreads, kAppend ? 3 : 5) kv4_rows_kernel(const Kv4Rows p) {
   const int lane = threadIdx.x & 31, sub = lane & 7, team = lane >> 3;
   const unsigned team_mask = 0xFFu << (8 * team);
-  const int heads = p.geom.heads;
+  const uint32_t heads = p.geom.heads, vecs = 2 * heads;   // keys of all heads, then values
   const int warps = static_cast<int>(gridDim.x) * (kKvThreads / 32);
   grid_dependency_wait();
   for (int64_t row64 = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5); row64 < p.seqs.rows;
@@ -71,49 +73,55 @@ __global__ void __launch_bounds__(kKvThreads) kv4_rows_kernel(const Kv4Rows p) {
     const int row = static_cast<int>(row64);
     const int64_t vec0 = kv4_row_vector(p, row);
     if (vec0 < 0) continue;
-    // keys of all heads, then values of all heads
-    for (int64_t first = blockIdx.y * kKv4RowVecs; first < 2 * static_cast<int64_t>(heads);
-         first += gridDim.y * kKv4RowVecs) {
+    __half *k_row = p.k + row * p.k_token, *v_row = p.v + row * p.v_token;
+    for (uint32_t first = blockIdx.y * kKv4RowVecs; first < vecs; first += gridDim.y * kKv4RowVecs) {
+      // (a team without a vector reads the last one once more, and stores nothing)
+      auto index = [&](int u) {
+        const uint32_t i = first + 4 * u + team;
+        return i < vecs ? i : vecs - 1;
+      };
       uint4 a[4], b[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int64_t i = first + 4 * u + team;
+        const uint32_t i = index(u);
         const bool value = i >= heads;
         const int head = static_cast<int>(value ? i - heads : i);
-        if (i >= 2 * static_cast<int64_t>(heads)) continue;   // the same for a team's lanes
         if constexpr (kAppend) {
-          const __half *x = (value ? p.v + row * p.v_token + head * p.v_head
-                                   : p.k + row * p.k_token + head * p.k_head) + sub * 16;
-          a[u] = __ldg(reinterpret_cast<const uint4 *>(x));
-          b[u] = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              (value ? v_row + head * p.v_head : k_row + head * p.k_head) + sub * 16);
+          a[u] = __ldg(src);
+          b[u] = __ldg(src + 1);
         } else {
           const int64_t vec = vec0 + static_cast<int64_t>(head) * p.geom.head_stride;
           // words `sub` and 8 + `sub`, so that a team writes 128 bytes in one piece
-          const uint32_t *q = reinterpret_cast<const uint32_t *>((value ? p.v4 : p.k4) + vec * 64) + sub;
-          a[u] = make_uint4(__ldg(q), __ldg(q + 8), __float_as_uint(__ldg((value ? p.vs : p.ks) + vec)), 0u);
+          const uint32_t *q =
+              reinterpret_cast<const uint32_t *>((value ? p.v4 : p.k4) + vec * 64) + sub;
+          a[u] = make_uint4(__ldg(q), __ldg(q + 8),
+                            __float_as_uint(__ldg((value ? p.vs : p.ks) + vec)), 0u);
         }
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int64_t i = first + 4 * u + team;
-        const bool value = i >= heads;
+        const uint32_t i = index(u);
+        const bool value = i >= heads, store = first + 4 * u + team < vecs;
         const int head = static_cast<int>(value ? i - heads : i);
-        if (i >= 2 * static_cast<int64_t>(heads)) continue;
         if constexpr (kAppend) {
           const int64_t vec = vec0 + static_cast<int64_t>(head) * p.geom.head_stride;
           const uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
           float scale;
-          *reinterpret_cast<uint2 *>((value ? p.v4 : p.k4) + vec * 64 + sub * 8) =
-              kv_encode16(w, team_mask, scale);
-          if (sub == 0) (value ? p.vs : p.ks)[vec] = scale;
+          const uint2 codes = kv_encode16(w, team_mask, scale);
+          if (store)
+            *reinterpret_cast<uint2 *>((value ? p.v4 : p.k4) + vec * 64 + sub * 8) = codes;
+          if (store && sub == 0) (value ? p.vs : p.ks)[vec] = scale;
         } else {
           uint32_t o[8];
           kv_decode16(make_uint2(a[u].x, a[u].y), __uint_as_float(a[u].z), o);
           uint4 *dst = reinterpret_cast<uint4 *>(
-              (value ? p.v + row * p.v_token + head * p.v_head
-                     : p.k + row * p.k_token + head * p.k_head) + sub * 8);
-          dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          dst[8] = make_uint4(o[4], o[5], o[6], o[7]);
+              value ? v_row + head * p.v_head : k_row + head * p.k_head) + sub;
+          if (store) {
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[8] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
       }
     }

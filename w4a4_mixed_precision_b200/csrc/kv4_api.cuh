@@ -5,7 +5,7 @@
 namespace {
 
 bool kv4_fits(int64_t v) { return v <= INT32_MAX; }
-// Rows leave room for the loops that step past them in 32 bits.
+// Rows and heads leave room for the loops that step past them in 32 bits.
 bool kv4_fits_rows(int64_t v) { return v <= atomk::kKv4MaxPositions; }
 
 // Sizes and strides, then (with `touched`) pointers.
@@ -14,7 +14,7 @@ atom_status_t kv4_check_cache(const atom_kv4_cache_t *c, bool touched) {
       c->head_stride < 0)
     return ATOM_ERR_INVALID_ARG;
   if (c->page_size < 1 || c->heads < 1 || !kv4_fits(c->pages) || !kv4_fits(c->page_size) ||
-      !kv4_fits(c->heads) || !kv4_fits(c->page_stride) || !kv4_fits(c->token_stride) ||
+      !kv4_fits_rows(c->heads) || !kv4_fits(c->page_stride) || !kv4_fits(c->token_stride) ||
       !kv4_fits(c->head_stride))
     return ATOM_ERR_SHAPE;
   if (!touched) return ATOM_OK;
@@ -141,10 +141,11 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
   p.k_head = k_head;
   p.v_token = v_token;
   p.v_head = v_head;
-  // a warp a row (and 16 of its vectors), eight CTAs an SM
+  // a warp a row (and 16 of its vectors); 15 CTAs an SM, a multiple of the three
+  // or five that it holds at once
   const int64_t ctas = (rows + atomk::kKvThreads / 32 - 1) / (atomk::kKvThreads / 32);
   const int64_t parts = (2 * cache->heads + atomk::kKv4RowVecs - 1) / atomk::kKv4RowVecs;
-  const int64_t cap = static_cast<int64_t>(dev->sm_count) * 8;
+  const int64_t cap = static_cast<int64_t>(dev->sm_count) * 15;
   const int grid_x = static_cast<int>(ctas < cap ? ctas : cap);
   int64_t grid_y = cap / grid_x;
   if (grid_y > parts) grid_y = parts;
