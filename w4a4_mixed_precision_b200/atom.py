@@ -694,11 +694,11 @@ def atom_kv4_gather(cache: KV4Cache, batch: KV4Batch, rows: int,
     shape = (rows, cache.heads, 128)
 
     def call(s):
-        out = [_kv4_output(t, cache.k4, torch.float16, shape, n, device)
-               for t, n in ((k, "k"), (v, "v"))]
+        to_k = _kv4_output(k, cache.k4, torch.float16, shape, "k", device)
+        to_v = _kv4_output(v, to_k, torch.float16, shape, "v", device)
         _check("atom_kv4_gather", lib().atom_kv4_gather(
-            cache._ref, batch._ref, rows, out[0].data_ptr(), out[1].data_ptr(), s))
-        return tuple(out)
+            cache._ref, batch._ref, rows, to_k.data_ptr(), to_v.data_ptr(), s))
+        return to_k, to_v
 
     return _kv4_run(device, stream, call)
 
