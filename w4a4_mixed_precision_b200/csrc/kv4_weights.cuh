@@ -226,71 +226,101 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
         had_head = u.head;
       }
       float *to = p.sums + (static_cast<int64_t>(u.b) * p.geom.heads + u.head) * p.width + tok0;
+      // keys of 16 tokens as A fragments: rows g and g + 8
+      auto expand = [&](int row, uint32_t (&kf)[8][4]) {
+        const uint4 ka = *reinterpret_cast<const uint4 *>(st + row * 64 + t * 16);
+        const uint4 kb = *reinterpret_cast<const uint4 *>(st + (row + 8) * 64 + t * 16);
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-      for (int q = 0; q < kTok; q += 32) {
-        float v[4];   // sums of the tokens 8 i + g
+        for (int j = 0; j < 4; ++j) {
+          uint32_t ca[4], cb[4];
+          codes_f16_word(wa[j], p.magic, ca);
+          codes_f16_word(wb[j], p.magic, cb);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // 16 tokens: rows g and g + 8 of the fragments
-          const int row = q + 16 * h + g;
-          const uint4 ka = *reinterpret_cast<const uint4 *>(st + row * 64 + t * 16);
-          const uint4 kb = *reinterpret_cast<const uint4 *>(st + (row + 8) * 64 + t * 16);
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-          uint32_t kf[8][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t ca[4], cb[4];
-            codes_f16_word(wa[j], p.magic, ca);
-            codes_f16_word(wb[j], p.magic, cb);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              kf[2 * j + k][0] = ca[2 * k];
-              kf[2 * j + k][1] = cb[2 * k];
-              kf[2 * j + k][2] = ca[2 * k + 1];
-              kf[2 * j + k][3] = cb[2 * k + 1];
-            }
-          }
-          const float s0 = sc[row] * p.scale_log2, s1 = sc[row + 8] * p.scale_log2;
-          // (sums of sums: the rounding of long ones stays small)
-          float sum[2] = {0.f, 0.f}, far[2] = {0.f, 0.f};
-          for (int r0 = first; r0 < rows; r0 += 8) {
-            if (rows > 8) {
-              queries(r0, rows);
-              had_b = -1;
-            }
-            float x[4] = {};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) mma_f16_16816(x, kf[k], qf[2 * k], qf[2 * k + 1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = exp2_approx(fmaf(x[e], e < 2 ? s0 : s1, -lse[e & 1]));
-            if (tok0 + q + 32 > least) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (tok0 + row + 8 * (e >> 1) >= limit[e & 1]) x[e] = 0.f;
-            }
-            sum[0] += x[0] + x[1];
-            sum[1] += x[2] + x[3];
-            if (((r0 >> 3) & 31) == 31) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                far[i] += sum[i];
-                sum[i] = 0.f;
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float w = far[i] + sum[i];
-            w += __shfl_xor_sync(0xffffffffu, w, 1);
-            w += __shfl_xor_sync(0xffffffffu, w, 2);
-            v[2 * h + i] = w;
+          for (int k = 0; k < 2; ++k) {
+            kf[2 * j + k][0] = ca[2 * k];
+            kf[2 * j + k][1] = cb[2 * k];
+            kf[2 * j + k][2] = ca[2 * k + 1];
+            kf[2 * j + k][3] = cb[2 * k + 1];
           }
         }
-        // lane (g, t) stores token 8 t + g
+      };
+      // weights of 16 tokens for 8 query rows
+      auto weigh = [&](const uint32_t (&kf)[8][4], int row, float s0, float s1, bool mask,
+                       float (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_f16_16816(x, kf[k], qf[2 * k], qf[2 * k + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = exp2_approx(fmaf(x[e], e < 2 ? s0 : s1, -lse[e & 1]));
+        if (mask) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (tok0 + row + 8 * (e >> 1) >= limit[e & 1]) x[e] = 0.f;
+        }
+      };
+      auto over_columns = [](float w) {
+        w += __shfl_xor_sync(0xffffffffu, w, 1);
+        return w + __shfl_xor_sync(0xffffffffu, w, 2);
+      };
+      // lane (g, t) stores token 8 t + g of 32, v: sums of the tokens 8 i + g
+      auto store = [&](int q, const float (&v)[4]) {
         const int tok = q + 8 * t + g;
         float w = t < 2 ? (t == 0 ? v[0] : v[1]) : (t == 2 ? v[2] : v[3]);
         if (p.prev != nullptr) w += sc[kTok + tok];
         if (tok0 + tok < u.s.len) to[tok] = w;
+      };
+      if (rows <= 8) {   // (without the loop over rows: 64 sequences of 8192 tokens: 77 us with it, 64
+                         // without)
+        const bool mask = tok0 + kTok > least;
+#pragma unroll
+        for (int q = 0; q < kTok; q += 32) {
+          float v[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = q + 16 * h + g;
+            uint32_t kf[8][4];
+            expand(row, kf);
+            float x[4];
+            weigh(kf, row, sc[row] * p.scale_log2, sc[row + 8] * p.scale_log2, mask, x);
+            v[2 * h] = over_columns(x[0] + x[1]);
+            v[2 * h + 1] = over_columns(x[2] + x[3]);
+          }
+          store(q, v);
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < kTok; q += 32) {
+          float v[4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = q + 16 * h + g;
+            uint32_t kf[8][4];
+            expand(row, kf);
+            const float s0 = sc[row] * p.scale_log2, s1 = sc[row + 8] * p.scale_log2;
+            // (sums of sums: the rounding of long ones stays small)
+            float sum[2] = {0.f, 0.f}, far[2] = {0.f, 0.f};
+            for (int r0 = first; r0 < rows; r0 += 8) {
+              queries(r0, rows);
+              had_b = -1;
+              float x[4];
+              weigh(kf, row, s0, s1, tok0 + q + 32 > least, x);
+              sum[0] += x[0] + x[1];
+              sum[1] += x[2] + x[3];
+              if (((r0 >> 3) & 31) == 31) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  far[i] += sum[i];
+                  sum[i] = 0.f;
+                }
+              }
+            }
+            v[2 * h] = over_columns(far[0] + sum[0]);
+            v[2 * h + 1] = over_columns(far[1] + sum[1]);
+          }
+          store(q, v);
+        }
       }
     }
     if (--left == 0) break;
