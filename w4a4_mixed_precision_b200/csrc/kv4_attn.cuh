@@ -22,10 +22,13 @@
 //
 // What bounds it: 136 bytes per cached token and KV head (64 + 4 each of keys
 // and values) against 4 * 128 * rows operations, far below the tensor cores'
-// balance for the at most 16 rows taken here. So the matrix instructions are
+// balance for the tiles of 8 or 16 rows taken here. So the matrix instructions are
 // warp-wide mma.sync, whose operands are made in registers from the loaded
 // words, with no expanded copy of a tile in shared memory (which a tcgen05
-// operand would need: twice the loaded bytes written, then read).
+// operand would need: twice the loaded bytes written, then read). It measures
+// 4.1 TB/s (64 sequences of up to 8192 tokens, 64 heads over 8: 419 MB in 102
+// us), with a warp's 300 instructions for 16 tokens, half of them turning codes
+// into fp16, and the twelve warps an SM that the rings leave room for.
 //
 // The products. M is the side of the tokens (first product) or of the elements
 // (second), N is the query rows, 8 per n-tile. A contraction's order is free,
