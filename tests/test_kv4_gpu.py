@@ -518,6 +518,45 @@ def test_a_sequence_listed_twice():
     assert torch.equal(out[:2], out[2:]) and torch.equal(lse[:2], lse[2:])
 
 
+@pytest.mark.parametrize("layout", ["heads first", "one head", "one token", "wide"])
+@pytest.mark.parametrize("new,heads", [([1, 4, 30], 2), ([150] * 10, 5)])
+def test_layouts_of_queries_keys_and_values(new, heads, layout):
+    """Row tensors whose strides are not a contiguous tensor's, broadcast ones among them."""
+    c = Call(67, new, [200 + i for i in range(len(new))], q_heads=2 * heads, heads=heads, page=16,
+             q_size=0.05, garbage=1.0)
+
+    def laid_out(a):
+        t = dev(a)
+        if layout == "heads first":
+            t = t.transpose(0, 1).contiguous().transpose(0, 1)
+        elif layout == "one head":
+            t = t[:, :1].expand(t.shape)
+        elif layout == "one token":
+            t = t[:1].expand(t.shape)
+        else:
+            wide = torch.zeros((t.shape[0], t.shape[1] + 3, 136), dtype=t.dtype, device="cuda")
+            wide[:, 1:-2, :128] = t
+            t = wide[:, 1:-2, :128]
+        return t, host(t)
+
+    (q, qn), (k, kn), (v, vn) = map(laid_out, (c.q, c.k, c.v))
+    cache, batch = c.device_cache(), c.device_batch()
+    atom.atom_kv4_append(k, v, cache, batch)
+    want = [a.copy() for a in c.cache]
+    ko.append(kn, vn, want, *c.sequences())
+    for got, ref in zip((cache.k4, cache.ks, cache.v4, cache.vs), want):
+        assert np.array_equal(host(got), ref)
+    out, lse = atom.atom_kv4_attention(q, cache, batch)
+    ref = ko.attention(qn, want, *c.sequences(), True, SCALE)
+    assert_within(host(out), ref[0], ref[1], "out")
+    assert_within(host(lse), ref[2], ref[3], "lse")
+    sums = torch.zeros((len(new), heads, 220), device="cuda")
+    atom.atom_kv4_attention_weights(q, lse, cache, batch, sums)
+    s, tol = ko.attention_weights(qn, host(lse), want, *c.sequences(), True, SCALE, 220)
+    inside = np.broadcast_to(np.arange(220)[None, None] < c.lens[:, None, None], s.shape)
+    assert_within(host(sums)[inside], s[inside], tol[inside], "sums")
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05])
 @pytest.mark.parametrize("new,heads", [([1, 3], 2), ([150] * 10, 5)])
 def test_scales_of_zero_and_below(scale, new, heads):

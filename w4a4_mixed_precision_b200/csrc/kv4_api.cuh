@@ -193,7 +193,8 @@ atom_status_t kv4_decode_ctas(DeviceState *dev, int nt, int *ctas) {
 bool kv4_query_map(CUtensorMap *map, const void *q, int64_t q_token, int64_t q_head, int64_t rows,
                    int64_t q_heads, int group) {
   EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
+  // (a tensor map's strides are not zero)
+  if (!fn || (q_heads > 1 && q_head == 0) || (rows > 1 && q_token == 0)) return false;
   // (a dimension of one has no stride of its own)
   const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(q_heads), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(q_heads > 1 ? q_head * 2 : 256),
