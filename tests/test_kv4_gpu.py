@@ -486,6 +486,59 @@ def test_weights_of_a_sequence_without_new_tokens():
     assert torch.equal(sums[..., :300], prev[..., :300]) and bool((sums[..., 300:] == 7).all())
 
 
+def test_between_the_quantizer_and_the_gemm():
+    """Layers of a step in one stream, whose kernels' set-ups may overlap: quantize, project
+    (the GEMM for few tokens, which holds tensor memory as the prompt kernels do), append,
+    attention and weights by the prompt kernels, the next layer's quantizer on the output."""
+    K, heads, group = 512, 5, 32
+    c = Call(70, [5] * 12, [300 + i for i in range(12)], q_heads=heads * group, heads=heads, page=16,
+             garbage=1.0)
+    cache, batch = c.device_cache(), c.device_batch()
+    first = [t.clone() for t in (cache.k4, cache.ks, cache.v4, cache.vs)]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    idx = torch.arange(0, 256, 2, dtype=torch.int32, device="cuda")
+    x0 = torch.randn((60, K), generator=gen, device="cuda").half()
+    w = torch.randn(((group + 2) * heads * 128, K), generator=gen, device="cuda").half() * 0.02
+    qw = atom.atom_quant_weights(w, idx)
+    ws = atom.gemm_workspace(60, w.shape[0], K, "cuda")
+
+    def step(between):
+        x, sums = x0, torch.zeros((12, heads, 320), device="cuda")
+        for _ in range(3):
+            qa = atom.atom_reorder_quant(x, idx)
+            between()
+            y = atom.atom_w4a4_gemm(qa, qw, K, workspace=ws).view(60, -1, 128)
+            between()
+            q, k, v = y.split([heads * group, heads, heads], 1)
+            atom.atom_kv4_append(k, v, cache, batch)
+            between()
+            out, lse = atom.atom_kv4_attention(q, cache, batch)
+            between()
+            atom.atom_kv4_attention_weights(q, lse, cache, batch, sums, prev=sums)
+            between()
+            x = out.view(60, -1)[:, :K]
+        return out, lse, sums
+
+    def restart():
+        for t, f in zip((cache.k4, cache.ks, cache.v4, cache.vs), first):
+            t.copy_(f)
+
+    want = [t.clone() for t in step(torch.cuda.synchronize)]
+    assert bool(want[0].isfinite().all())
+    for _ in range(5):
+        restart()
+        for a, b in zip(step(lambda: None), want):
+            assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(lambda: None)
+    for _ in range(5):
+        restart()
+        graph.replay()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_two_streams_at_once():
     """The same work on two streams at a time, each call with its own workspace."""
     cases = [Call(60, [1] * 5, [700, 3, 2000, 64, 900], page=16, q_size=0.05),
