@@ -143,11 +143,17 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
                       is ? 4u : 0u);
         }
         const uint8_t *kp = p.k4 + lane_code + vec * 64;
+        if (n >= kTok && step == 512) {   // (a head's tokens together need no address sums: 64 -> 63 us)
 #pragma unroll
-        for (int i = 0; i < kTok / 8; ++i) {
-          const bool is = 8 * i + g < n;
-          cp_async_16(k_dst + at + i * 512, is ? kp : p.k4, is ? 16u : 0u);
-          kp += step;
+          for (int i = 0; i < kTok / 8; ++i)
+            cp_async_16(k_dst + at + i * 512, kp + i * 512, 16u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTok / 8; ++i) {
+            const bool is = 8 * i + g < n;
+            cp_async_16(k_dst + at + i * 512, is ? kp : p.k4, is ? 16u : 0u);
+            kp += step;
+          }
         }
       } else {
         for (int j = 0; j < kTok; j += 32) {
