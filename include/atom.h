@@ -445,6 +445,7 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *     limit = kv_len, or with causal != 0: kv_len - qn + i + 1,
  *     lse = log sum_t exp(s[t]),  out = fp16( sum_t exp(s[t] - lse) v[t] ),
  *   with k, v = code * scale unrounded. limit <= 0: out 0, lse -infinity.
+ *   |scale| <= 1e18 (else ATOM_ERR_INVALID_ARG).
  *   out fp16 [rows][q_heads][128], lse fp32 [rows][q_heads] or NULL.
  *   workspace: scratch that lets a sequence's cached tokens be shared between
  *   CTAs; at least atom_kv4_attention_workspace_bytes(rows, q_heads, heads,

@@ -610,6 +610,18 @@ def test_layouts_of_queries_keys_and_values(new, heads, layout):
     assert_within(host(sums)[inside], s[inside], tol[inside], "sums")
 
 
+@pytest.mark.parametrize("new,heads", [([1, 3], 2), ([150] * 10, 5)])
+def test_the_largest_scale(new, heads):
+    """One token takes all (its score is 1e17 above the next), and nothing overflows."""
+    c = Call(68, new, [200 + i for i in range(len(new))], q_heads=2 * heads, heads=heads, page=16,
+             garbage=1.0)
+    out, lse = atom.atom_kv4_attention(dev(c.q), c.device_cache(), c.device_batch(), scale=1e18)
+    want = ko.attention(c.q, c.cache, *c.sequences(), True, 1e18)
+    lse, ref = host(lse), want[2]
+    assert np.isfinite(host(out)).all()
+    assert (np.abs(lse - ref) <= np.abs(ref) * 2.0 ** -20 + want[3]).all()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05])
 @pytest.mark.parametrize("new,heads", [([1, 3], 2), ([150] * 10, 5)])
 def test_scales_of_zero_and_below(scale, new, heads):

@@ -310,6 +310,12 @@ def q4(*lead):
     return torch.zeros(*lead, 64, dtype=torch.uint8)
 
 
+@pytest.mark.parametrize("scale", [1.1e18, -1e30, float("inf"), float("nan")])
+def test_scales_that_scores_cannot_hold_are_refused(lib, scale):
+    assert attention(lib, scale=scale) == INVALID
+    assert weights(lib, scale=scale) == INVALID
+
+
 def test_more_rows_than_2_to_30_are_refused(lib):
     assert append(lib, rows=2 ** 30 + 1) == SHAPE
     assert attention(lib, rows=2 ** 30 + 1, q_heads=2) == SHAPE

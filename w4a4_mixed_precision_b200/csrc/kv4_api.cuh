@@ -222,7 +222,9 @@ atom_status_t kv4_check_queries(int64_t rows, int64_t q_heads, float scale,
                                 const atom_kv4_cache_t *cache, const atom_kv4_batch_t *batch,
                                 bool *touched) {
   if (rows < 0 || q_heads < 0) return ATOM_ERR_INVALID_ARG;
-  if (!(scale - scale == 0.f)) return ATOM_ERR_INVALID_ARG;   // not finite
+  // With vectors of fp16 numbers no score times log2(e) then passes 1e30, which
+  // stands for a row that has seen nothing (kKv4NoMax).
+  if (!(fabsf(scale) <= 1e18f)) return ATOM_ERR_INVALID_ARG;
   *touched = rows > 0 && batch != nullptr && batch->batch > 0;
   atom_status_t st;
   if ((st = kv4_check_cache(cache, *touched)) != ATOM_OK) return st;
