@@ -42,7 +42,7 @@
 // two warps taking turns at the exponentials (337 against 334), the next tile's
 // scores read ahead (356 against 334).
 //
-// Operand layouts. K and V tiles are 128 rows (tokens) of 256 bytes as two
+// Operand layouts. K and V tiles are 64 rows (tokens) of 256 bytes as two
 // halves of 128-byte rows with the 128-byte swizzle: for S they are a K-major B
 // operand, for O an MN-major one. A word of 8 codes becomes one 16-byte chunk:
 // of keys in its own order, as the queries are copied; of values in the order
