@@ -422,7 +422,9 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *                included (they are its last).
  *   cu_q         int32 [batch + 1]: rows cu_q[b] .. cu_q[b+1] - 1 of the call's
  *                row tensors are the new tokens of sequence b. Rows behind
- *                cu_q[batch] (padding) are neither read nor written.
+ *                cu_q[batch] (padding) are not written, and what they hold, NaN
+ *                and infinities included, changes nothing; so it is with the
+ *                queries of a sequence that has nothing cached.
  *   max_q        host bound on cu_q[b+1] - cu_q[b]: picks the kernels that read
  *                queries. (A larger one costs time only.)
  * A sequence whose entries contradict the call (cu_q descending or above the
@@ -457,10 +459,11 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *     sums[b][h][t] = prev[b][h][t] + sum over sequence b's new tokens and the
  *                     query heads of h of exp(s[t] - lse)       for t < kv_len
  *   with q, lse, causal and scale as given to and returned by
- *   atom_kv4_attention; a row with lse = -infinity adds nothing. prev fp32
- *   [batch][heads][width] (may be sums itself), or NULL: 0. Elements t >= kv_len
- *   are left as they are. kv_len > width sets the device status, like the
- *   contradictions above. No atomics: the result is the same every time.
+ *   atom_kv4_attention; a row with lse = -infinity adds nothing, whatever its
+ *   query holds. prev fp32 [batch][heads][width] (may be sums itself), or NULL:
+ *   0. Elements t >= kv_len are left as they are. kv_len > width sets the device
+ *   status, like the contradictions above. No atomics: the result is the same
+ *   every time.
  *
  * atom_kv4_evict: per sequence and KV head, new_len = min(kv_len, budget)
  *   tokens stay: the last min(recent, new_len), and of the others those with the

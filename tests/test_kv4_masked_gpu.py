@@ -1,0 +1,104 @@
+"""The paged INT4 KV cache's operators on the GPU beside what they must not see: padding and idle
+rows, rows that count for nothing, cached tokens behind a row's own."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4_oracle as ko
+from w4a4_mixed_precision_b200 import atom
+
+from kv4_util import Call, assert_within, dev, host
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 128 ** -0.5
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    atom.atom_device_status(clear=True)
+    yield
+    assert atom.atom_device_status(clear=True) == 0
+
+
+def check_weights(c, q, lse, causal=True, prev=None, lse_ref=None):
+    """The sums of queries `q` against the oracle's of c.q, and the elements behind the lengths."""
+    width = int(c.lens.max()) + 3
+    shape = (len(c.lens), c.heads, width)
+    sums = torch.full(shape, 7.0, device="cuda")
+    atom.atom_kv4_attention_weights(q, lse, c.device_cache(), c.device_batch(), sums, causal=causal)
+    want, tol = ko.attention_weights(c.q, host(lse) if lse_ref is None else lse_ref, c.cache,
+                                     *c.sequences(), causal, SCALE, width)
+    inside = np.broadcast_to(np.arange(width)[None, None] < c.lens[:, None, None], shape)
+    assert_within(host(sums)[inside], want[inside], tol[inside], "sums")
+    assert (host(sums)[~inside] == 7).all()
+    return sums
+
+
+@pytest.mark.parametrize("fill", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,lens,q_heads,heads", [
+    ([1, 3], [40, 90], 8, 2),
+    ([1, 1, 2, 1], [200, 0, 77, 0], 8, 8),
+    ([200], [700], 16, 2),
+    ([9], [9], 7, 1),
+    ([150, 1, 40, 1, 133], [150, 0, 300, 0, 500], 10, 5),
+    ([150, 7, 20] * 4, [400, 7, 300] * 4, 35, 5),
+])
+def test_what_padding_and_idle_rows_hold_counts_for_nothing(new, lens, q_heads, heads, causal, fill):
+    """Query, key and value rows behind the last sequence, and the query of a slot with nothing
+    cached, hold NaN or infinities."""
+    c = Call(81, new, lens, q_heads=q_heads, heads=heads, page=16, pad_rows=150, q_size=0.05,
+             garbage=1.0)
+    n = int(c.cu_q[-1])
+    idle = np.zeros(c.rows, bool)
+    for b in np.flatnonzero(c.lens == 0):
+        idle[c.cu_q[b]:c.cu_q[b + 1]] = True
+    nothing = idle | (np.arange(c.rows) >= n)
+    q, k, v = (x.copy() for x in (c.q, c.k, c.v))
+    for x in (q, k, v):
+        x[nothing] = fill
+    cache, batch = c.device_cache(), c.device_batch()
+    if not idle.any():
+        atom.atom_kv4_append(dev(k), dev(v), cache, batch)
+        ko.append(c.k, c.v, c.cache, *c.sequences())
+        for got, ref in zip((cache.k4, cache.ks, cache.v4, cache.vs), c.cache):
+            assert np.array_equal(host(got), ref)
+        back = [torch.full((c.rows, heads, 128), 7.0, dtype=torch.float16, device="cuda")
+                for _ in range(2)]
+        atom.atom_kv4_gather(cache, batch, c.rows, *back)
+        for got, ref in zip(back, ko.gather(c.cache, *c.sequences(), c.rows)):
+            assert np.array_equal(host(got)[:n], ref[:n]) and (host(got)[n:] == 7).all()
+    out = torch.full((c.rows, q_heads, 128), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((c.rows, q_heads), 7.0, device="cuda")
+    atom.atom_kv4_attention(dev(q), cache, batch, causal=causal, out=out, lse=lse)
+    want = ko.attention(c.q, c.cache, *c.sequences(), causal, SCALE)
+    assert_within(host(out)[:n], want[0][:n], want[1][:n], "out")
+    assert_within(host(lse)[:n], want[2][:n], want[3][:n], "lse")
+    assert (host(out)[n:] == 7).all() and (host(lse)[n:] == 7).all()
+    sums = check_weights(c, dev(q), lse, causal)
+    # by sums that such rows have no part in the same tokens stay
+    budget = max(1, int(c.lens.max()) // 2)
+    kept_ref, lens_ref = ko.evict(host(sums), c.lens, budget, 3 if budget > 3 else 0)
+    new_lens = torch.empty(len(new), dtype=torch.int32, device="cuda")
+    kept, _ = atom.atom_kv4_evict(sums, cache, batch, budget, 3 if budget > 3 else 0, cache,
+                                  batch.block_table, new_lens)
+    assert np.array_equal(host(kept), kept_ref) and np.array_equal(host(new_lens), lens_ref)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,lens,q_heads,heads", [
+    ([1, 6], [40, 90], 4, 4), ([9, 5], [60, 400], 12, 2), ([300], [700], 16, 2),
+    ([150, 30, 128], [150, 300, 500], 10, 5),
+])
+def test_rows_without_a_log_sum_exp_count_for_nothing(new, lens, q_heads, heads, causal):
+    """A row whose lse is -infinity adds nothing, whatever its query holds."""
+    c = Call(82, new, lens, q_heads=q_heads, heads=heads, page=24, q_size=0.05)
+    _, lse = atom.atom_kv4_attention(dev(c.q), c.device_cache(), c.device_batch(), causal=causal)
+    rng = np.random.default_rng(4)
+    silent = rng.random((c.rows, q_heads)) < 0.2
+    silent[-1, -1] = True
+    z, q = host(lse).copy(), c.q.copy()
+    z[silent] = -np.inf
+    q[silent] = np.where(rng.random((int(silent.sum()), 1)) < 0.5, np.nan, np.inf)
+    check_weights(c, dev(q), dev(z), causal)

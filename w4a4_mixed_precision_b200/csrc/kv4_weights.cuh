@@ -207,10 +207,10 @@ kv4_weights_kernel(const __grid_constant__ Kv4Weights p) {
         const int qc = kv4_div(rc, p.by_group);
         const float z = __ldg(p.lse + static_cast<int64_t>(u.s.q0 + qc) * p.q_heads +
                               u.head * p.group + rc - qc * p.group);
-        if (z != -INFINITY) {   // (a row that saw nothing)
-          limit[c] = kv4_limit(u.s, qc, p.causal != 0);
-          lse[c] = z * 1.44269504088896341f;
-        }
+        // (a row that saw nothing is masked too: its query may hold anything)
+        const bool some = z != -INFINITY;
+        limit[c] = some ? kv4_limit(u.s, qc, p.causal != 0) : 0;
+        if (some) lse[c] = z * 1.44269504088896341f;
       }
     }
     least = __reduce_min_sync(0xffffffffu, limit[0] < limit[1] ? limit[0] : limit[1]);
@@ -414,7 +414,8 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
   using namespace kv4_wprompt_cfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem);   // [kStages] query tile stored
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem);   // [kStages] rows that count for nothing
+                                                           // cleared, log-sum-exps stored
   uint64_t *q_empty = q_full + kStages;     // [kStages] its product complete
   uint64_t *s_full = q_empty + kStages;     // [kBufs] product complete
   uint64_t *s_empty = s_full + kBufs;       // [kBufs] product read
@@ -425,14 +426,16 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
   uint64_t *item_full = sum_empty + 2;      // [kItems]
   uint64_t *item_empty = item_full + kItems;
   uint64_t *done = item_empty + kItems;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  uint64_t *q_copied = done + 1;            // [kStages] query tile copied
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_copied + kStages);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   Kv4WItem *ring = reinterpret_cast<Kv4WItem *>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&q_full[i], 4);      // one arrival per warp, here and below (+ the copies' bytes)
+      mbar_init(&q_full[i], 4);      // one arrival per warp, here and below
+      mbar_init(&q_copied[i], 1);    // + the copies' bytes
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < kBufs; ++i) {
@@ -584,7 +587,7 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
     // ================================================================ load
     const int lt = threadIdx.x - 32 * kLoadWarp;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    uint32_t tiles = 0, items = 0;
+    uint32_t tiles = 0, items = 0, copies = 0;   // copies: tiles whose copies were started
     for (;;) {
       Kv4WItem it;
       if (!(ok = take_item(it)) || !it.more) break;
@@ -651,24 +654,41 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
         // this tile's stage, of tile t + 12, waited until product t + 9 was read, so
         // the warps that take t's turn are past it)
         reinterpret_cast<float *>(smem + kLseOff)[(tiles % kLseStages) * kRows + lt] = -z;
-        __syncwarp();
         if (lt == 0) {
-          mbar_arrive_expect_tx(&q_full[st], p.tile_rows * 256);
+          mbar_arrive_expect_tx(&q_copied[st], p.tile_rows * 256);
           const int tok = it.q0 + kv4_div(it.row0 + i * p.tile_rows, p.by_group);
           for (int h = 0; h < 2; ++h)
             tma_load_3d(smem + kQOff + st * kTile + h * kHalf, &q_map, 64 * h, it.head * p.group,
-                        tok, &q_full[st]);
-        } else if (lane == 0) {
-          mbar_arrive(&q_full[st]);
+                        tok, &q_copied[st]);
         }
+        ++copies;
+        // A row that counts for nothing may hold anything (the copy of a sequence's
+        // last tile also brings the rows behind it), and a score of NaN minus an
+        // infinite log-sum-exp is still NaN: its elements are cleared. (Selecting in
+        // the sums instead, for tiles with such rows alone, took the 4096-token
+        // prompt, which has none, from 192 us to 236.)
+        const bool clear = z == INFINITY && lt < p.tile_rows;
+        if (__any_sync(0xffffffffu, clear)) {
+          ok = mbar_wait_idle(&q_copied[st], (tiles / kStages) & 1, abort_flag, 20);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (clear) {
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c)
+              st_shared_v4(smem + kQOff + st * kTile + (c >> 3) * kHalf + lt * 128 + (c & 7) * 16, 0u,
+                           0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[st]);
       }
       if (!ok) break;
       ++items;
     }
     // copies in flight land before shared memory is released
     if (!ok && lt == 0)
-      for (uint32_t no = tiles > kStages ? tiles - kStages : 0; no < tiles; ++no)
-        (void)mbar_wait(&q_full[no % kStages], (no / kStages) & 1, nullptr);
+      for (uint32_t no = copies > kStages ? copies - kStages : 0; no < copies; ++no)
+        (void)mbar_wait(&q_copied[no % kStages], (no / kStages) & 1, nullptr);
     if (!ok && lane == 0) fail();
   } else if (warp == kMmaWarp) {
     // ================================================================ MMA issuer
@@ -683,6 +703,7 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
       for (int i = 0; ok && i < it.tiles; ++i, ++tiles) {
         const uint32_t st = tiles % kStages, buf = tiles % kBufs;
         ok = mbar_wait(&s_empty[buf], ((tiles / kBufs) & 1) ^ 1u, abort_flag) &&
+             mbar_wait(&q_copied[st], (tiles / kStages) & 1, abort_flag) &&
              mbar_wait(&q_full[st], (tiles / kStages) & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
