@@ -102,3 +102,26 @@ def test_rows_without_a_log_sum_exp_count_for_nothing(new, lens, q_heads, heads,
     z[silent] = -np.inf
     q[silent] = np.where(rng.random((int(silent.sum()), 1)) < 0.5, np.nan, np.inf)
     check_weights(c, dev(q), dev(z), causal)
+
+
+@pytest.mark.parametrize("new,group", [(2, 128), (1, 100)])
+def test_weights_of_a_prefix_beyond_2_to_31_query_rows(new, group):
+    """A sequence whose cached tokens before the new ones, times the group's query heads, pass
+    2^31: all of them are seen by every row. (Its pages are one page, listed again and again.)"""
+    page = 64
+    pages = 2 ** 31 // group // page + 17
+    c = Call(83, [new], [page], q_heads=group, heads=1, page=page, q_size=0.05)
+    length = pages * page
+    table = torch.full((1, pages), int(c.table[0, 0]), dtype=torch.int32, device="cuda")
+    batch = atom.KV4Batch(table, dev(np.array([length], np.int32)), dev(c.cu_q), max_q=new)
+    z = ko.attention(c.q, c.cache, *c.sequences(), False, SCALE)[2] + np.log(pages)
+    z = z.astype(np.float32)
+    sums = torch.full((1, 1, length), 7.0, device="cuda")
+    atom.atom_kv4_attention_weights(dev(c.q), dev(z), c.device_cache(), batch, sums)
+    want, tol = ko.attention_weights(c.q, z, c.cache, *c.sequences(), False, SCALE, page)
+    got = sums.view(pages, page)
+    assert_within(host(got[0]), want[0, 0], tol[0, 0], "sums")
+    assert bool((got[:-1] == got[0]).all())
+    # the last page holds the new tokens: the last of them only the last query sees
+    want, tol = ko.attention_weights(c.q, z, c.cache, *c.sequences(), True, SCALE, page)
+    assert_within(host(got[-1]), want[0, 0], tol[0, 0], "last page")

@@ -505,8 +505,9 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
       if (!(ok = take_item(it)) || !it.more) break;
       const int pos = it.tok0 + tid;
       const bool valid = pos < it.len;
-      // first row that sees the token
-      const int sees = p.causal ? (pos - (it.len - it.qn)) * p.group : 0;
+      // first row that sees the token (a prefix times the group can pass 2^31)
+      const int first_qi = pos - (it.len - it.qn);
+      const int sees = p.causal && first_qi > 0 ? first_qi * p.group : 0;
       ok = mbar_wait_idle(&k_full[items & 1], (items >> 1) & 1, abort_flag, 32);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const float k = reinterpret_cast<const float *>(smem + kKsOff)[(items & 1) * kTok + tid];
