@@ -125,3 +125,33 @@ def test_weights_of_a_prefix_beyond_2_to_31_query_rows(new, group):
     # the last page holds the new tokens: the last of them only the last query sees
     want, tol = ko.attention_weights(c.q, z, c.cache, *c.sequences(), True, SCALE, page)
     assert_within(host(got[-1]), want[0, 0], tol[0, 0], "last page")
+
+
+@pytest.mark.parametrize("size", [2.0 ** -14, 0.0])
+@pytest.mark.parametrize("new,lens,q_heads,heads", [
+    ([3, 5, 2], [3, 60, 129], 4, 4),
+    ([4, 4], [64, 50], 8, 2),
+    ([2, 8], [31, 200], 1, 1),
+    ([60], [60], 16, 2),
+    ([150] * 8, [400, 300, 150, 210, 333, 230, 1000, 151], 8, 8),
+    ([1000], [1100], 7, 1),
+])
+def test_values_behind_a_row_leave_its_output_alone(new, lens, q_heads, heads, size):
+    """Later tokens' value scales up to 2^27 times a row's own, or beside zeros (all of them as fp16
+    vectors have them): the row does not see them, and its weights keep their precision."""
+    c = Call(84, new, lens, q_heads=q_heads, heads=heads, page=16, q_size=0.05, garbage=1.0)
+    unit = (c.cache[3] / c.cache[3].max()).astype(np.float32)
+    c.cache[3] = unit * np.float32(size)
+    want = ko.attention(c.q, c.cache, *c.sequences(), True, SCALE)
+    later = [a.copy() for a in c.cache]
+    rows = np.zeros(c.rows, bool)            # those that see none of the large values
+    for b, n in enumerate(c.new):
+        few = (n + 1) // 2
+        at = np.arange(c.lens[b] - few, c.lens[b])
+        place = (c.table[b, at // 16], at % 16)
+        later[3][place] = unit[place] * np.float32(2.0 ** 13)
+        rows[c.cu_q[b]:c.cu_q[b + 1] - few] = True
+    assert rows.any()
+    out, lse = atom.atom_kv4_attention(dev(c.q), c.device_cache(later), c.device_batch())
+    assert_within(host(out)[rows], want[0][rows], want[1][rows], "out")
+    assert_within(host(lse)[rows], want[2][rows], want[3][rows], "lse")

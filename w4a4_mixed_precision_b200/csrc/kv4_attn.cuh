@@ -17,8 +17,11 @@
 // of (its largest x among them) + e, x = s log2(e): the weight 2^(x + e - R + 4)
 // vs 2^-e is then at most 2^15 (R lags by up to 11 before the sums are rescaled)
 // whatever the scales are. It keeps fp16's full precision down to 2^-18 of R's
-// own, and an absolute error of 2^-29 of the tokens' largest value below. The
-// sum of weights uses the same reference.
+// own, and an absolute error of 2^-29 of the tokens' largest value below. Where a
+// row does not see all of the 64 tokens, R follows its largest x + log2 vs
+// instead (the weights' bound is the same): with e, a token that the row does not
+// see, its value scale 2^28 times the others', left them 2^-24 of themselves,
+// fp16's last bit. The sum of weights uses the same reference.
 //
 // What bounds it: 136 bytes per cached token and KV head (64 + 4 each of keys
 // and values) against 4 * 128 * rows operations, far below the tensor cores'
@@ -100,6 +103,16 @@ __device__ __forceinline__ int kv4_exponent(uint32_t bits) {
 __device__ __forceinline__ float kv4_down(int e) {
   return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
+
+// log2 of a value scale that has been multiplied by 2^-e, at least `least`: with e
+// not below -60, as e itself is not, and with any e not below -100 (the weights
+// are summed in units of 2^e: a token's is then below 2^115).
+__device__ __forceinline__ float kv4_level(float scaled, float least) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(scaled));
+  return fmaxf(y, least);
+}
+__device__ __forceinline__ float kv4_least_level(float e) { return fmaxf(-60.f - e, -100.f); }
 
 namespace kv4_decode_cfg {
 constexpr int kThreads = 128;
@@ -579,29 +592,46 @@ kv4_decode_kernel(const __grid_constant__ Kv4Attn p) {
             x[n][h][3] *= s1;
           }
         }
-        // the least limit differs between lanes: each masks what it must
-        if (tok0 + kTok > least) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int h = 0; h < kTok / 16; ++h)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (tok0 + 16 * h + g + 8 * (e >> 1) >= limit[n][e & 1]) x[n][h][e] = -INFINITY;
-        }
         const int e = kv4_exponent(__reduce_max_sync(
             0xffffffffu, __float_as_uint(fmaxf(sc[kTok + lane], sc[kTok + 32 + lane]))));
         const float ef = static_cast<float>(e), down = kv4_down(e);
-        // the references of the columns
+        // what the references of the columns follow
         float mx[NT][2];
+        if (__any_sync(0xffffffffu, tok0 + kTok > least)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
+          const float least_level = kv4_least_level(ef);
+#pragma unroll
+          for (int h = 0; h < kTok / 16; ++h)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int row = 16 * h + 8 * k + g;
+              const float level = kv4_level(sc[kTok + row] * down, least_level);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  if (tok0 + row >= limit[n][c]) x[n][h][2 * k + c] = -INFINITY;
+                  mx[n][c] = fmaxf(mx[n][c], x[n][h][2 * k + c] + level);
+                }
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float v = fmaxf(x[n][0][c], x[n][0][c + 2]);
+#pragma unroll
+              for (int h = 1; h < kTok / 16; ++h) v = max3(v, x[n][h][c], x[n][h][c + 2]);
+              mx[n][c] = v;
+            }
+        }
         bool rise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float v = fmaxf(x[n][0][c], x[n][0][c + 2]);
-#pragma unroll
-            for (int h = 1; h < kTok / 16; ++h) v = max3(v, x[n][h][c], x[n][h][c + 2]);
+            float v = mx[n][c];
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));

@@ -248,9 +248,10 @@ __device__ __forceinline__ Kv4Item kv4_prompt_item(const Kv4Attn &p, int &b, int
 }
 
 // A row's scores of a KV tile in the exponent's units (x, -infinity where the
-// row does not see), and the largest, each plus its e: what the reference
-// follows. `sc`, in shared memory: ks, vs (scaled by 2^-e) and the e's, one per
-// 32 tokens. (A tile of 64 also keeps this code, unrolled, short enough for the
+// row does not see), and what the reference follows: the largest of each 32
+// tokens plus their e, or (kMask) the largest x + log2 vs, to which tokens that
+// the row does not see add nothing. `sc`, in shared memory: ks, vs (scaled by
+// 2^-e) and the e's, one per 32 tokens. (A tile of 64 also keeps this code, unrolled, short enough for the
 // instruction caches beside that of the other roles; at 128 columns half of the
 // softmax's time went into waiting for instructions.)
 template <bool kMask>
@@ -281,6 +282,12 @@ __device__ __forceinline__ float kv4_row_scores(uint32_t s_addr, const float4 *s
           if (left <= 1) y.y = -INFINITY;
         }
         x[16 * c + 2 * i + h] = y;
+        if (kMask) {
+          const float4 v = sc[kTok / 4 + 8 * c + i];
+          const float least = kv4_least_level(c == 0 ? e.x : e.y);
+          y = f2_add(y, make_float2(kv4_level(h == 0 ? v.x : v.z, least),
+                                    kv4_level(h == 0 ? v.y : v.w, least)));
+        }
         m4[2 * (i & 1) + h] = max3(m4[2 * (i & 1) + h], y.x, y.y);
       }
     }
