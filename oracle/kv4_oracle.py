@@ -71,9 +71,10 @@ def attention(q, cache, table, kv_lens, cu_q, causal, scale):
     p |v| as much as the weights may be off: a score's error e makes 2e of weight and total, an
     exponential 2^-21, a weight p vs rounded to fp16 2^-11, sums of n terms made 16 at a time and
     over four or more partial sums (n / 16 + 64) 2^-24. A weight below fp16's normal range is off
-    by half its smallest step, 2^-25, in units in which 2^4 stands for the weight of the row's
-    largest score times the power of two above the largest value scale: of n codes of at most 7,
-    n * 7 * 2^-29 * 2 max vs."""
+    by half its smallest step, 2^-25, in units in which 2^4 stands for the largest, over the 64
+    tokens that share them and those before, of what the row sees: its largest weight there times
+    the power of two above the largest value scale there. Of the row's n codes of at most 7 that is
+    at most n * 7 * 2^-29 * 2 max(p vs)."""
     k4, ks, v4, vs = cache
     rows, hq = q.shape[:2]
     group = hq // k4.shape[2]
@@ -101,9 +102,12 @@ def attention(q, cache, table, kv_lens, cu_q, causal, scale):
             out[mine, head] = p @ v
             e = np.where(seen, err, 0).max(-1)
             off = 2 * e + 2.0 ** -21 + 2.0 ** -11 + (length / 16 + 64) * 2.0 ** -24
-            floor = length * 7 * 2.0 ** -28 * vsc[:, h].max()
-            out_tol[mine, head] = (np.abs(out[mine, head]) * 2.0 ** -11 + 2.0 ** -25 + floor +
-                                   off[:, None] * (p @ np.abs(v)))
+            groups = np.arange(0, length, 64)
+            largest = (np.maximum.reduceat(p, groups, -1) *
+                       np.maximum.reduceat(np.where(seen, vsc[:, h], 0), groups, -1)).max(-1)
+            floor = seen.sum(-1) * 7 * 2.0 ** -28 * largest
+            out_tol[mine, head] = (np.abs(out[mine, head]) * 2.0 ** -11 + 2.0 ** -25 +
+                                   floor[:, None] + off[:, None] * (p @ np.abs(v)))
             lse[mine, head] = np.where(some, top[:, 0] + np.log(np.where(some, total[:, 0], 1)),
                                        -np.inf)
             lse_tol[mine, head] = np.where(
