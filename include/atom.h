@@ -480,9 +480,9 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *   cu_q and max_q are not read. budget >= 1, 0 <= recent <= budget,
  *   new_width >= budget.
  *
- * Every entry: rows, batch 0: no-op. Sizes above 2^31 - 1, rows, heads or query
- * rows of a KV head above 2^30, a page_size < 1, q_heads not a multiple of heads:
- * ATOM_ERR_SHAPE. Inputs must be finite where they are read; slots behind a
+ * Every entry: rows, batch 0: no-op. Sizes above 2^31 - 1, rows, heads, sequences
+ * or query rows of a KV head above 2^30, a page_size < 1, q_heads not a multiple
+ * of heads: ATOM_ERR_SHAPE. Inputs must be finite where they are read; slots behind a
  * sequence's last token may hold anything. Outputs share no memory with inputs
  * or each other, but as said above. Stream-ordered, allocates nothing.
  */

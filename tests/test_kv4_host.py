@@ -323,6 +323,12 @@ def test_more_rows_than_2_to_30_are_refused(lib):
     assert weights(lib, rows=2 ** 29 + 1, q_heads=4) == SHAPE
 
 
+def test_more_sequences_than_2_to_30_are_refused(lib):
+    """Searches add two sequence numbers, and threads round runs of them up, in 32 bits."""
+    for n in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert both(lib, dict(b=batch(batch=n))) == (SHAPE,) * 4
+
+
 def test_binding_checks_a_cache():
     s = torch.zeros(3, 16, 2)
     with pytest.raises(ValueError, match="CUDA"):

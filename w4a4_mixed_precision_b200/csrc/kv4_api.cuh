@@ -5,7 +5,8 @@
 namespace {
 
 bool kv4_fits(int64_t v) { return v <= INT32_MAX; }
-// Rows and heads leave room for the loops that step past them in 32 bits.
+// Rows, heads and sequences leave room for the loops that step past them, and sums
+// of two of them, in 32 bits.
 bool kv4_fits_rows(int64_t v) { return v <= atomk::kKv4MaxPositions; }
 
 // Sizes and strides, then (with `touched`) pointers.
@@ -54,7 +55,7 @@ atom_status_t kv4_check_table(const int32_t *table, int64_t stride, int64_t max_
 
 atom_status_t kv4_check_batch(const atom_kv4_batch_t *b, bool rows_read) {
   if (!b || b->batch < 0 || b->max_q < 0) return ATOM_ERR_INVALID_ARG;
-  if (!kv4_fits(b->batch)) return ATOM_ERR_SHAPE;
+  if (!kv4_fits_rows(b->batch)) return ATOM_ERR_SHAPE;
   if (b->batch == 0) return ATOM_OK;
   const atom_status_t st = kv4_check_table(b->block_table, b->table_stride, b->max_pages);
   if (st != ATOM_OK) return st;
