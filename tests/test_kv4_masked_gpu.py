@@ -155,3 +155,25 @@ def test_values_behind_a_row_leave_its_output_alone(new, lens, q_heads, heads, s
     out, lse = atom.atom_kv4_attention(dev(c.q), c.device_cache(later), c.device_batch())
     assert_within(host(out)[rows], want[0][rows], want[1][rows], "out")
     assert_within(host(lse)[rows], want[2][rows], want[3][rows], "lse")
+
+
+def test_evict_with_the_largest_budget():
+    """A budget of 2^31 - 1: every token stays, and the rest of `kept` is -1."""
+    budget = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 24 * 2 ** 30:
+        pytest.skip("needs 24 GB")
+    c = Call(85, [0], [5000], q_heads=1, heads=1, page=16)
+    to = Call(86, [0], [5000], q_heads=1, heads=1, page=64)
+    dst = to.device_cache()
+    w = np.random.default_rng(1).random((1, 1, 5001)).astype(np.float32)
+    new_lens = torch.empty(1, dtype=torch.int32, device="cuda")
+    kept, new_w = atom.atom_kv4_evict(dev(w), c.device_cache(), c.device_batch(), budget, 100, dst,
+                                      dev(to.table), new_lens)
+    assert host(new_lens).tolist() == [5000]
+    assert np.array_equal(host(kept[0, 0, :5000]), np.arange(5000))
+    assert int(kept[0, 0, 5000:].max()) == int(kept[0, 0, 5000:].min()) == -1
+    assert np.array_equal(host(new_w[0, 0, :5000]), w[0, 0, :5000])
+    at = np.arange(5000)
+    for x, ref in zip((dst.k4, dst.ks, dst.v4, dst.vs), c.cache):
+        assert np.array_equal(host(x)[to.table[0, at // 64], at % 64],
+                              ref[c.table[0, at // 16], at % 16])

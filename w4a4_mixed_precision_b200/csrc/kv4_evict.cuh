@@ -304,7 +304,8 @@ kv4_evict_kernel(const __grid_constant__ Kv4Evict p, const int cluster_size) {
     }
   }
   for (int i = old + rank * T + tid; i < len; i += cluster * T) kept[want + i - old] = i;
-  for (int i = new_len + rank * T + tid; i < p.budget; i += cluster * T) kept[i] = -1;
+  for (int64_t i = new_len + rank * T + tid; i < p.budget; i += cluster * T)   // (to 2^31 - 1)
+    kept[i] = -1;
   sync_all();
 
   // ---- move them. A warp takes 32 tokens at a time: a lane finds the addresses
