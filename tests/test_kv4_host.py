@@ -37,6 +37,36 @@ int64_t part_begin(int64_t total, int parts, int i) { return kv4_part_begin(tota
 int capacity(int64_t max_pages, int64_t page_size) { return kv4_capacity(max_pages, page_size); }
 int64_t few_rows(int64_t pairs, int64_t max_rows, int sms) { return kv4_few_rows(pairs, max_rows, sms); }
 
+// Items' query copies with a wait for an empty buffer that gives up at its
+// give_up-th call (0: none does). 0: every copy was started in a buffer that was
+// empty, and what was under way at the end was waited for.
+int query_copies(int items, int give_up) {
+  uint32_t started[2] = {0, 0};
+  int waits = 0, copies[2] = {0, 0}, landed[2] = {0, 0}, bad = 0;
+  bool ok = true;
+  for (int i = 0; ok && i < items; ++i)
+    ok = kv4_start_queries(
+        started,
+        [&](int w, uint32_t parity) {
+          // a buffer is empty when its last copy has landed and been used; the
+          // barrier's phase before the first reads as odd
+          bad |= parity != ((copies[w] & 1u) ^ 1u);
+          if (++waits == give_up) return false;
+          landed[w] = copies[w];
+          return true;
+        },
+        [&](int w) {
+          bad |= landed[w] != copies[w];
+          ++copies[w];
+        });
+  bad |= ok != (give_up == 0 || give_up > 2 * items);
+  kv4_drain_queries(started, [&](int w, uint32_t parity) {
+    bad |= copies[w] == 0 || parity != ((copies[w] - 1u) & 1u);
+    landed[w] = copies[w];
+  });
+  return bad || landed[0] != copies[0] || landed[1] != copies[1];
+}
+
 // The decode kernel's division of a call among `ctas` CTAs, walked through on
 // the host. Counts how often every (tile, unit) is computed, checks that a
 // tile's shares are exactly the slots that its join reads, and returns 0 where
@@ -184,6 +214,12 @@ def test_parts_of_long_lines(plan):
         edges = [plan.part_begin(total, 592, i) for i in range(593)]
         assert edges[0] == 0 and edges[-1] == total
         assert all(b - a in (total // 592, total // 592 + 1) for a, b in zip(edges, edges[1:]))
+
+
+def test_query_copies_are_waited_for_wherever_a_wait_gives_up(plan):
+    for items in range(1, 6):
+        for give_up in range(0, 2 * items + 2):
+            assert plan.query_copies(items, give_up) == 0, (items, give_up)
 
 
 # ------------------------------------------------------------------------------ refusals

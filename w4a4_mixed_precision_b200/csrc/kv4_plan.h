@@ -138,6 +138,26 @@ inline int64_t kv4_few_rows(int64_t pairs, int64_t max_rows, int sms) {
   }
   return rows;
 }
+// The copies of an item's two query tiles, each into a buffer of its own as soon
+// as that is empty. started[w]: copies into buffer w so far; each completes one
+// phase of the buffer's barrier. False: a wait gave up, with what was started
+// before it still under way.
+template <class Wait, class Start>
+KV4_HD bool kv4_start_queries(uint32_t (&started)[2], const Wait &wait_empty, const Start &start) {
+  for (int w = 0; w < 2; ++w) {
+    if (!wait_empty(w, (started[w] & 1) ^ 1u)) return false;
+    start(w);
+    ++started[w];
+  }
+  return true;
+}
+// Waits until none of them is under way.
+template <class Wait>
+KV4_HD void kv4_drain_queries(const uint32_t (&started)[2], const Wait &wait_full) {
+  for (int w = 0; w < 2; ++w)
+    if (started[w] > 0) wait_full(w, (started[w] - 1) & 1);
+}
+
 // Sort key of an accumulated weight: larger weights have larger keys, the two
 // zeros the same, NaN the smallest.
 KV4_HD uint32_t kv4_weight_key(uint32_t bits) {

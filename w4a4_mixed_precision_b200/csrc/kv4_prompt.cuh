@@ -633,7 +633,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       if (warp == kQWarp && lane == 0) {
         int b = line.b, turn = 0;
         int64_t place = blockIdx.x, rest = line.rest;
-        uint32_t loads = 0;
+        uint32_t started[2] = {0, 0};
         bool ok = true;
         const uint32_t bytes = p.tile_rows * 256;
         for (uint32_t made = 0;; ++made) {
@@ -653,22 +653,26 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
           mbar_arrive(&item_empty[slot]);   // as one of its readers
           if (!it.more) break;
           if (it.kv_tiles == 0) continue;
-          for (int w = 0; w < 2; ++w) {
-            if (!(ok = mbar_wait_idle(&q_empty[w], (loads & 1) ^ 1u, abort_flag, 32))) break;
-            mbar_arrive_expect_tx(&q_full[w], bytes);
-            const int tok = it.q0 + kv4_div(it.row0 + p.tile_rows * w, p.by_group);
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(smem + kQOff + w * kQTile + h * kQHalf, &q_map, 64 * h, it.head * p.group,
-                          tok, &q_full[w]);
-          }
+          ok = kv4_start_queries(
+              started,
+              [&](int w, uint32_t parity) {
+                return mbar_wait_idle(&q_empty[w], parity, abort_flag, 32);
+              },
+              [&](int w) {
+                mbar_arrive_expect_tx(&q_full[w], bytes);
+                const int tok = it.q0 + kv4_div(it.row0 + p.tile_rows * w, p.by_group);
+                for (int h = 0; h < 2; ++h)
+                  tma_load_3d(smem + kQOff + w * kQTile + h * kQHalf, &q_map, 64 * h,
+                              it.head * p.group, tok, &q_full[w]);
+              });
           if (!ok) break;
-          ++loads;
         }
         if (!ok) {
           fail();
           // copies in flight land before shared memory is released
-          for (int w = 0; w < 2; ++w)
-            if (loads > 0) (void)mbar_wait(&q_full[w], (loads - 1) & 1, nullptr);
+          kv4_drain_queries(started, [&](int w, uint32_t parity) {
+            (void)mbar_wait(&q_full[w], parity, nullptr);
+          });
         }
       }
     } else {
