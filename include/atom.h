@@ -451,7 +451,8 @@ ATOM_API atom_status_t atom_kv_dequant(const uint8_t *q4, const float *scales, i
  *   out fp16 [rows][q_heads][128], lse fp32 [rows][q_heads] or NULL.
  *   workspace: scratch that lets a sequence's cached tokens be shared between
  *   CTAs; at least atom_kv4_attention_workspace_bytes(rows, q_heads, heads,
- *   max_q), 16-byte aligned, contents irrelevant before and after. NULL, or
+ *   max_q), 16-byte aligned, contents irrelevant before and after (0 bytes: no
+ *   rows, sizes that the call refuses, or a CUDA call that failed). NULL, or
  *   fewer bytes: no sharing (same result up to the fp32 summation order). Two
  *   calls that overlap on the GPU must not share a workspace.
  *

@@ -406,3 +406,16 @@ def test_binding_checks_rows():
         atom._kv4_rows(torch.zeros(4, 2, 128), 2, "q", None)
     with pytest.raises(ValueError, match="CUDA"):
         atom._kv4_rows(torch.zeros(4, 2, 128, dtype=torch.float16), 2, "q", None)
+
+
+def test_a_failed_workspace_query_is_raised_and_not_kept(monkeypatch):
+    answers = [0, 4096]
+    monkeypatch.setattr(atom, "atom_kv4_attention_workspace_bytes", lambda *a: answers.pop(0))
+    sizes = (2 ** 20, 5, 8, 2, 7)          # a device that no other test names
+    with pytest.raises(atom.AtomError, match="ATOM_ERR_CUDA"):
+        atom._kv4_workspace_bytes(*sizes)
+    assert atom._kv4_workspace_bytes(*sizes) == atom._kv4_workspace_bytes(*sizes) == 4096
+    # no work, or sizes that the call itself refuses
+    monkeypatch.setattr(atom, "atom_kv4_attention_workspace_bytes", lambda *a: 0)
+    for rows, q_heads, heads, max_q in [(0, 8, 2, 7), (5, 7, 2, 7), (5, 8, 2, 0), (5, 0, 2, 7)]:
+        assert atom._kv4_workspace_bytes(2 ** 20 + 1, rows, q_heads, heads, max_q) == 0

@@ -708,8 +708,14 @@ def atom_kv4_attention_workspace_bytes(rows: int, q_heads: int, heads: int, max_
 
 
 @functools.lru_cache(maxsize=64)
-def _kv4_workspace_bytes(device_index: int, *sizes: int) -> int:
-    return atom_kv4_attention_workspace_bytes(*sizes)   # of the current device, device_index
+def _kv4_workspace_bytes(device_index: int, rows: int, q_heads: int, heads: int,
+                         max_q: int) -> int:
+    """Of the current device, device_index. 0 says that there is no work, sizes that the call
+    refuses, or a failed CUDA call: that one raises, and is not kept."""
+    n = atom_kv4_attention_workspace_bytes(rows, q_heads, heads, max_q)
+    if n == 0 and min(rows, q_heads, heads, max_q) > 0 and q_heads % heads == 0:
+        _check("atom_kv4_attention_workspace_bytes", 5)   # ATOM_ERR_CUDA
+    return n
 
 
 def atom_kv4_attention(q: torch.Tensor, cache: KV4Cache, batch: KV4Batch, causal: bool = True,
