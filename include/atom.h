@@ -553,15 +553,16 @@ ATOM_API atom_status_t atom_probe_mma_i8(int64_t groups, int32_t *pairs_out,
 
 /*
  * atom_debug_wait_timeout -- a test aid for the library's failure detection
- * (the pages have no counterpart). Every pipeline wait in the GEMM and
- * quantizer kernels is bounded: a wait that runs past its limit gives up,
- * records ATOM_ERR_TIMEOUT in the device status word and lets the kernel end,
- * instead of hanging the GPU. This entry point runs that same bounded wait
- * (the same device function) in a one-thread kernel on an mbarrier that
- * nothing ever arrives on and that no copy or MMA is tied to, with a limit of
- * `limit_ns` nanoseconds in place of the production 1 s. The kernel therefore
- * gives up after about `limit_ns`, and the next atom_device_status() reports
- * ATOM_ERR_TIMEOUT. Nothing is left in flight; the context stays usable.
+ * (the pages have no counterpart). Every pipeline wait of the library's kernels
+ * is bounded: a wait that runs past its limit gives up, records ATOM_ERR_TIMEOUT
+ * in the device status word and lets the kernel end, instead of hanging the GPU.
+ * This entry point runs those same bounded waits (the same device functions:
+ * by a timer, and two that count looks, which the paged cache's prompt kernels
+ * take) in one small kernel on an mbarrier that nothing ever arrives on and that
+ * no copy or MMA is tied to, with a limit of `limit_ns` nanoseconds in place of
+ * the production 1 s. The kernel therefore ends after about `limit_ns`, and the
+ * next atom_device_status() reports ATOM_ERR_TIMEOUT if all of them gave up.
+ * Nothing is left in flight; the context stays usable.
  *
  *   limit_ns  0 < limit_ns <= 1e9 (else ATOM_ERR_INVALID_ARG).
  * Stream-ordered, allocates nothing.

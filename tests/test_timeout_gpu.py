@@ -40,3 +40,16 @@ def test_bounded_wait_gives_up_and_reports_timeout(c_oracle):
     assert y_rel_err(y, c_oracle.gemm(*ra, *rw, K)) <= Y_TOL
     assert atom.atom_device_status(clear=True) == 0
 
+
+@pytest.mark.parametrize("limit_ns", [1_000, 300_000_000])
+def test_waits_that_count_looks_end_near_their_limit(limit_ns):
+    """The status is set once the timed wait and both that count looks have given up: all of them
+    do so within some times the limit."""
+    assert atom.atom_device_status(clear=True) == 0
+    t0 = time.perf_counter()
+    atom.atom_debug_wait_timeout(limit_ns)
+    status = atom.atom_device_status(clear=True)             # synchronises
+    elapsed = time.perf_counter() - t0
+    assert atom.STATUS[status] == "ATOM_ERR_TIMEOUT"
+    assert limit_ns * 1e-9 <= elapsed < limit_ns * 4e-9 + 0.5
+    assert atom.atom_device_status(clear=True) == 0

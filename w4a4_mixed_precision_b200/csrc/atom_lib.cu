@@ -851,7 +851,8 @@ atom_status_t atom_debug_wait_timeout(uint64_t limit_ns, atom_stream_t stream) {
   DeviceState *dev = nullptr;
   const atom_status_t st = current_device(&dev);
   if (st != ATOM_OK) return st;
-  atomk::wait_timeout_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(limit_ns);
+  atomk::wait_timeout_kernel<<<1, atomk::kWaitTimeoutThreads, 0,
+                               reinterpret_cast<cudaStream_t>(stream)>>>(limit_ns);
   return cudaGetLastError() == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
 

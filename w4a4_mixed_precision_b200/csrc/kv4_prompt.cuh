@@ -131,31 +131,10 @@ __device__ __forceinline__ uint32_t desc_lo_mn(uint32_t saddr, uint32_t lbo) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
-// Bounded wait that leaves the issue slots to the other warps: a first look,
-// then one every `ns` nanoseconds or so.
-__device__ __forceinline__ bool mbar_wait_idle(uint64_t *bar, uint32_t parity,
-                                               const volatile int *abort_flag, uint32_t ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  for (uint32_t i = 0; i < kWaitLimitNs / 32; ++i) {
-    __nanosleep(ns);
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-  }
-  return false;
-}
-
-// Bounded wait without a timer, which costs the softmax 2 per cent wherever it is
-// read (1x4096 prompt 323 us with it, 315 without): a look takes at least 20
-// clocks, and what is waited for here takes some microseconds. The roles that
-// issue the MMAs wait with a timer, and their giving up ends this wait too.
-__device__ __forceinline__ bool mbar_wait_spin(uint64_t *bar, uint32_t parity,
-                                               const volatile int *abort_flag) {
-  for (uint32_t i = 1; i <= 1u << 22; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0 && *abort_flag) return false;
-  }
-  return false;
-}
+// What the items of the persistent loops wait for can be as long as an item takes
+// (one of a cache of 2^26 tokens some seconds) or as finding one among many idle
+// sequences: 32 times the other waits' limit. A role that gives up ends them too.
+constexpr uint32_t kItemLooks = 32 * kWaitLooks;
 
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
@@ -405,7 +384,8 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   uint32_t item_no = 0;
   auto take_item = [&](Kv4Item &it) -> bool {
     const int slot = item_no % kItems;
-    const bool ok = mbar_wait_idle(&item_full[slot], (item_no / kItems) & 1, abort_flag, 64);
+    const bool ok =
+        mbar_wait_idle(&item_full[slot], (item_no / kItems) & 1, abort_flag, 64, kItemLooks);
     if (!__all_sync(0xffffffffu, ok)) return false;
     it = ring[slot];
     __syncwarp();
@@ -638,8 +618,8 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         const uint32_t bytes = p.tile_rows * 256;
         for (uint32_t made = 0;; ++made) {
           const int slot = made % kItems;
-          if (!(ok = mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64)))
-            break;
+          ok = mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64, kItemLooks);
+          if (!ok) break;
           Kv4Item it{};
           if (place < line.total) {
             it = kv4_prompt_item(p, b, rest);
@@ -656,7 +636,7 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
           ok = kv4_start_queries(
               started,
               [&](int w, uint32_t parity) {
-                return mbar_wait_idle(&q_empty[w], parity, abort_flag, 32);
+                return mbar_wait_idle(&q_empty[w], parity, abort_flag, 32, kItemLooks);
               },
               [&](int w) {
                 mbar_arrive_expect_tx(&q_full[w], bytes);

@@ -484,7 +484,8 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
   uint32_t item_no = 0;
   auto take_item = [&](Kv4WItem &it) -> bool {
     const int slot = item_no % kItems;
-    const bool ok = mbar_wait_idle(&item_full[slot], (item_no / kItems) & 1, abort_flag, 64);
+    const bool ok =
+        mbar_wait_idle(&item_full[slot], (item_no / kItems) & 1, abort_flag, 64, kItemLooks);
     if (!__all_sync(0xffffffffu, ok)) return false;
     it = ring[slot];
     __syncwarp();
@@ -733,7 +734,8 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
     int64_t place = blockIdx.x, rest = line.rest;
     for (uint32_t made = 0;; ++made) {
       const int slot = made % kItems;
-      if (!(ok = mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64))) break;
+      ok = mbar_wait_idle(&item_empty[slot], ((made / kItems) & 1) ^ 1u, abort_flag, 64, kItemLooks);
+      if (!ok) break;
       Kv4WItem it{};
       if (place < line.total) {
         it = kv4_wprompt_item(p, b, rest);
