@@ -142,17 +142,22 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
   p.k_head = k_head;
   p.v_token = v_token;
   p.v_head = v_head;
-  // a warp a row (and 16 of its vectors); 15 CTAs an SM, a multiple of the three
-  // or five that it holds at once
-  const int64_t ctas = (rows + atomk::kKvThreads / 32 - 1) / (atomk::kKvThreads / 32);
-  const int64_t parts = (2 * cache->heads + atomk::kKv4RowVecs - 1) / atomk::kKv4RowVecs;
-  const int64_t cap = static_cast<int64_t>(dev->sm_count) * 15;
+  const int64_t vecs = 2 * cache->heads, step = atomk::kKv4RowVecs;
+  p.by_vecs = static_cast<uint32_t>((65536 + vecs - 1) / vecs);
+  // 15 CTAs an SM, a multiple of the three or five that it holds at once
+  const int64_t cap = static_cast<int64_t>(dev->sm_count) * 15, warps = atomk::kKvThreads / 32;
+  const bool line = vecs % step != 0;   // (measured at the kernel)
+  // a warp 16 places of the line, or a row, whose parts of 16 grid_y may divide
+  const int64_t steps = line ? (rows * vecs + step - 1) / step : rows;
+  const int64_t ctas = (steps + warps - 1) / warps, parts = line ? 1 : vecs / step;
   const int grid_x = static_cast<int>(ctas < cap ? ctas : cap);
   int64_t grid_y = cap / grid_x;
   if (grid_y > parts) grid_y = parts;
+  void (*const fn)(atomk::Kv4Rows) =
+      append ? (line ? atomk::kv4_rows_kernel<true, true> : atomk::kv4_rows_kernel<true, false>)
+             : (line ? atomk::kv4_rows_kernel<false, true> : atomk::kv4_rows_kernel<false, false>);
   const cudaError_t err =
-      kv4_launch(append ? atomk::kv4_rows_kernel<true> : atomk::kv4_rows_kernel<false>,
-                 dim3(static_cast<unsigned>(grid_x), static_cast<unsigned>(grid_y), 1),
+      kv4_launch(fn, dim3(static_cast<unsigned>(grid_x), static_cast<unsigned>(grid_y), 1),
                  atomk::kKvThreads, 0, stream, p);
   return err == cudaSuccess ? ATOM_OK : ATOM_ERR_CUDA;
 }
