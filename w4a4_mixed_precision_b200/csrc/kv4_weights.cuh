@@ -360,7 +360,9 @@ constexpr uint32_t kQOff = 1024;
 constexpr uint32_t kLseOff = kQOff + kStages * kTile;
 constexpr uint32_t kKsOff = kLseOff + kLseStages * kRows * 4;   // [2][128] key scales
 constexpr uint32_t kSumOff = kKsOff + 2 * kTok * 4;             // [2][128] sums of half the tiles
-constexpr uint32_t kSmemBytes = kSumOff + 2 * kTok * 4 + 1024;  // + alignment slack
+constexpr uint32_t kNoneOff = kSumOff + 2 * kTok * 4;   // [kLseStages][4]: of 32 rows each, whether
+                                                        // one of the tile counts for nothing
+constexpr uint32_t kSmemBytes = kNoneOff + kLseStages * 16 + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemK = 0, kTmemS = 128;   // 2 x 64 columns of keys, 3 x 128 of products
 constexpr uint32_t kIdesc = idesc_f16(128, 128);
@@ -414,8 +416,7 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
   using namespace kv4_wprompt_cfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem);   // [kStages] rows that count for nothing
-                                                           // cleared, log-sum-exps stored
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem);   // [kStages] query tile stored
   uint64_t *q_empty = q_full + kStages;     // [kStages] its product complete
   uint64_t *s_full = q_empty + kStages;     // [kBufs] product complete
   uint64_t *s_empty = s_full + kBufs;       // [kBufs] product read
@@ -426,16 +427,14 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
   uint64_t *item_full = sum_empty + 2;      // [kItems]
   uint64_t *item_empty = item_full + kItems;
   uint64_t *done = item_empty + kItems;
-  uint64_t *q_copied = done + 1;            // [kStages] query tile copied
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_copied + kStages);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   Kv4WItem *ring = reinterpret_cast<Kv4WItem *>(tmem_slot + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&q_full[i], 4);      // one arrival per warp, here and below
-      mbar_init(&q_copied[i], 1);    // + the copies' bytes
+      mbar_init(&q_full[i], 4);      // one arrival per warp, here and below (+ the copies' bytes)
       mbar_init(&q_empty[i], 1);
     }
     for (int i = 0; i < kBufs; ++i) {
@@ -525,7 +524,42 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
         const float4 *lse = reinterpret_cast<const float4 *>(smem + kLseOff) +
                             (no % kLseStages) * (kRows / 4);
         const int from = sees - (it.row0 + i * p.tile_rows);   // first column that counts
-        const bool mask = __any_sync(0xffffffffu, from > 0);
+        // A row that counts for nothing may hold anything (the copy of a sequence's
+        // last tile also brings the rows behind it), and a score of NaN minus an
+        // infinite log-sum-exp is still NaN. Tiles with such rows, and those with rows
+        // that do not see all of the warp's tokens, select, in a short loop over the
+        // columns that the tile has: the loop below is the faster for having no
+        // selection in it. (Prompt of 4096 tokens 180 us; with the rows before `from`
+        // left to the loop below 188, with all selections there 225. Clearing the
+        // rows' elements before the product, for which the copy has to land first,
+        // took 16 sequences with 32 rows from 45 us to 65.)
+        const int4 none = reinterpret_cast<const int4 *>(smem + kNoneOff)[no % kLseStages];
+        if (__any_sync(0xffffffffu, from > 0 || (none.x | none.y | none.z | none.w) != 0)) {
+          const int rows = it.qn * p.group - (it.row0 + i * p.tile_rows);
+          const int columns = rows < p.tile_rows ? rows : p.tile_rows;
+          float own[4] = {};
+#pragma unroll 1
+          for (int c = 0; c < columns; c += 32) {
+            uint32_t r[32];
+            tmem_ld_x32(s_addr + c, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 z = lse[c / 4 + j];   // (behind `columns` -infinity too)
+              const float z4[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float y = fmaf(__uint_as_float(r[4 * j + e]), k, z4[e]);
+                own[e] += exp2_approx(c + 4 * j + e < from || z4[e] == -INFINITY ? -INFINITY : y);
+              }
+            }
+          }
+          sum += (own[0] + own[1]) + (own[2] + own[3]);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[buf]);
+          continue;
+        }
         float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t raw[2][32];
         tmem_ld_x32(s_addr, raw[0]);
@@ -550,10 +584,6 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
                                 k2, h == 0 ? make_float2(z.x, z.y) : make_float2(z.z, z.w));
               y.x = exp2_approx(y.x);
               y.y = exp2_approx(y.y);
-              if (mask) {
-                if (32 * c + 4 * j + 2 * h < from) y.x = 0.f;
-                if (32 * c + 4 * j + 2 * h + 1 < from) y.y = 0.f;
-              }
               part[h] = f2_add(part[h], y);
             }
           }
@@ -589,7 +619,7 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
     // ================================================================ load
     const int lt = threadIdx.x - 32 * kLoadWarp;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    uint32_t tiles = 0, items = 0, copies = 0;   // copies: tiles whose copies were started
+    uint32_t tiles = 0, items = 0;
     for (;;) {
       Kv4WItem it;
       if (!(ok = take_item(it)) || !it.more) break;
@@ -656,41 +686,27 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
         // this tile's stage, of tile t + 12, waited until product t + 9 was read, so
         // the warps that take t's turn are past it)
         reinterpret_cast<float *>(smem + kLseOff)[(tiles % kLseStages) * kRows + lt] = -z;
+        const bool some = __any_sync(0xffffffffu, z == INFINITY && lt < p.tile_rows);
+        if (lane == 0)
+          reinterpret_cast<int *>(smem + kNoneOff)[(tiles % kLseStages) * 4 + (warp & 3)] = some;
+        __syncwarp();
         if (lt == 0) {
-          mbar_arrive_expect_tx(&q_copied[st], p.tile_rows * 256);
+          mbar_arrive_expect_tx(&q_full[st], p.tile_rows * 256);
           const int tok = it.q0 + kv4_div(it.row0 + i * p.tile_rows, p.by_group);
           for (int h = 0; h < 2; ++h)
             tma_load_3d(smem + kQOff + st * kTile + h * kHalf, &q_map, 64 * h, it.head * p.group,
-                        tok, &q_copied[st]);
+                        tok, &q_full[st]);
+        } else if (lane == 0) {
+          mbar_arrive(&q_full[st]);
         }
-        ++copies;
-        // A row that counts for nothing may hold anything (the copy of a sequence's
-        // last tile also brings the rows behind it), and a score of NaN minus an
-        // infinite log-sum-exp is still NaN: its elements are cleared. (Selecting in
-        // the sums instead, for tiles with such rows alone, took the 4096-token
-        // prompt, which has none, from 192 us to 236.)
-        const bool clear = z == INFINITY && lt < p.tile_rows;
-        if (__any_sync(0xffffffffu, clear)) {
-          ok = mbar_wait_idle(&q_copied[st], (tiles / kStages) & 1, abort_flag, 20);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          if (clear) {
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c)
-              st_shared_v4(smem + kQOff + st * kTile + (c >> 3) * kHalf + lt * 128 + (c & 7) * 16, 0u,
-                           0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[st]);
       }
       if (!ok) break;
       ++items;
     }
     // copies in flight land before shared memory is released
     if (!ok && lt == 0)
-      for (uint32_t no = copies > kStages ? copies - kStages : 0; no < copies; ++no)
-        (void)mbar_wait(&q_copied[no % kStages], (no / kStages) & 1, nullptr);
+      for (uint32_t no = tiles > kStages ? tiles - kStages : 0; no < tiles; ++no)
+        (void)mbar_wait(&q_full[no % kStages], (no / kStages) & 1, nullptr);
     if (!ok && lane == 0) fail();
   } else if (warp == kMmaWarp) {
     // ================================================================ MMA issuer
@@ -705,7 +721,6 @@ kv4_weights_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
       for (int i = 0; ok && i < it.tiles; ++i, ++tiles) {
         const uint32_t st = tiles % kStages, buf = tiles % kBufs;
         ok = mbar_wait(&s_empty[buf], ((tiles / kBufs) & 1) ^ 1u, abort_flag) &&
-             mbar_wait(&q_copied[st], (tiles / kStages) & 1, abort_flag) &&
              mbar_wait(&q_full[st], (tiles / kStages) & 1, abort_flag);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after_sync();
