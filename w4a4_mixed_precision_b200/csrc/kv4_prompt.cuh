@@ -69,8 +69,8 @@ constexpr uint32_t kTile = kTok * 256, kHalf = kTile / 2;
 constexpr uint32_t kQOff = 1024;
 constexpr uint32_t kKOff = kQOff + 2 * kQTile;
 constexpr uint32_t kVOff = kKOff + kStages * kTile;
-constexpr uint32_t kScOff = kVOff + kStages * kTile;   // ks, vs of a tile's tokens, 2 exponents
-constexpr uint32_t kScStage = 2 * kTok * 4 + 16;
+constexpr uint32_t kScOff = kVOff + kStages * kTile;   // ks, vs of a tile's tokens, 2 exponents,
+constexpr uint32_t kScStage = 3 * kTok * 4 + 16;       // log2 of the vs
 constexpr uint32_t kOutOff = kScOff + kScStages * kScStage;      // 2 KB for each softmax warp
 constexpr uint32_t kSmemBytes = kOutOff + 8 * 2048 + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;
@@ -230,7 +230,7 @@ __device__ __forceinline__ Kv4Item kv4_prompt_item(const Kv4Attn &p, int &b, int
 // row does not see), and what the reference follows: the largest of each 32
 // tokens plus their e, or (kMask) the largest x + log2 vs, to which tokens that
 // the row does not see add nothing. `sc`, in shared memory: ks, vs (scaled by
-// 2^-e) and the e's, one per 32 tokens. (A tile of 64 also keeps this code, unrolled, short enough for the
+// 2^-e), the e's, one per 32 tokens, and kv4_level of the vs. (A tile of 64 also keeps this code, unrolled, short enough for the
 // instruction caches beside that of the other roles; at 128 columns half of the
 // softmax's time went into waiting for instructions.)
 template <bool kMask>
@@ -262,10 +262,8 @@ __device__ __forceinline__ float kv4_row_scores(uint32_t s_addr, const float4 *s
         }
         x[16 * c + 2 * i + h] = y;
         if (kMask) {
-          const float4 v = sc[kTok / 4 + 8 * c + i];
-          const float least = kv4_least_level(c == 0 ? e.x : e.y);
-          y = f2_add(y, make_float2(kv4_level(h == 0 ? v.x : v.z, least),
-                                    kv4_level(h == 0 ? v.y : v.w, least)));
+          const float4 v = sc[2 * kTok / 4 + 1 + 8 * c + i];
+          y = f2_add(y, h == 0 ? make_float2(v.x, v.y) : make_float2(v.z, v.w));
         }
         m4[2 * (i & 1) + h] = max3(m4[2 * (i & 1) + h], y.x, y.y);
       }
@@ -576,8 +574,10 @@ kv4_prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         if (value) {
           const uint32_t largest = __reduce_max_sync(0xffffffffu, __float_as_uint(scale));
           const int e = kv4_exponent(largest);
-          sc[kTok + 32 * ew + lane] = scale * kv4_down(e);
-          if (lane == 0) sc[2 * kTok + ew] = static_cast<float>(e);
+          const float ef = static_cast<float>(e), scaled = scale * kv4_down(e);
+          sc[kTok + 32 * ew + lane] = scaled;
+          sc[2 * kTok + 4 + 32 * ew + lane] = kv4_level(scaled, kv4_least_level(ef));
+          if (lane == 0) sc[2 * kTok + ew] = ef;
         } else {
           sc[32 * ew + lane] = scale * p.scale_log2;
         }
