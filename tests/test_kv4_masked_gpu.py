@@ -177,3 +177,21 @@ def test_evict_with_the_largest_budget():
     for x, ref in zip((dst.k4, dst.ks, dst.v4, dst.vs), c.cache):
         assert np.array_equal(host(x)[to.table[0, at // 64], at % 64],
                               ref[c.table[0, at // 16], at % 16])
+
+
+@pytest.mark.parametrize("share", [0.1, 0.5, 1.0])
+@pytest.mark.parametrize("most,spread,batch", [(8, 16, 1500), (160, 100, 24)])
+def test_zero_values_leave_the_log_sum_exp_its_bound(most, spread, batch, share):
+    """Tokens whose values are zero (a scale of 0, as the quantizer writes it) beside value scales
+    that jump from token to token, and nothing but such tokens."""
+    rng = np.random.default_rng(5)
+    new = rng.integers(most // 2 if most > 8 else 1, most + 1, batch)
+    c = Call(5, new, new + rng.integers(0, spread, batch), q_heads=8, heads=4, page=16, q_size=0.02,
+             garbage=1.0)
+    shape = c.cache[3].shape
+    jumping = c.cache[3] * np.exp2(rng.integers(-13, 9, shape))
+    c.cache[3] = np.where(rng.random(shape) < share, 0, np.minimum(jumping, 9000)).astype(np.float32)
+    out, lse = atom.atom_kv4_attention(dev(c.q), c.device_cache(), c.device_batch())
+    want = ko.attention(c.q, c.cache, *c.sequences(), True, SCALE)
+    assert_within(host(out), want[0], want[1], "out")
+    assert_within(host(lse), want[2], want[3], "lse")

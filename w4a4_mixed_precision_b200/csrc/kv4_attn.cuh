@@ -95,24 +95,30 @@ constexpr float kKv4NoMax = -1e30f;
 // 2^kKv4Lag behind the largest.
 constexpr float kKv4Raise = 4.f, kKv4Lag = 11.f;
 
-// Exponent e of a positive number's (its bits): the number < 2^e; and 2^-e.
+// Exponent e of a positive number's (its bits): the number < 2^e; and 2^-e. Not
+// below that of the smallest value scale but 0, 2^-24 / 7: references and sums stay
+// near 1, and a log-sum-exp, their two logarithms' sum, keeps its last bits (0.5 of
+// its bound where half of the values are zero; with -60 it passed that).
+constexpr int kKv4LeastExponent = -26;
 __device__ __forceinline__ int kv4_exponent(uint32_t bits) {
   const int e = static_cast<int>(bits >> 23) - 126;
-  return e < -60 ? -60 : (e > 100 ? 100 : e);
+  return e < kKv4LeastExponent ? kKv4LeastExponent : (e > 100 ? 100 : e);
 }
 __device__ __forceinline__ float kv4_down(int e) {
   return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
 // log2 of a value scale that has been multiplied by 2^-e, at least `least`: with e
-// not below -60, as e itself is not, and with any e not below -100 (the weights
-// are summed in units of 2^e: a token's is then below 2^115).
+// not below the least exponent, as e itself is not, and with any e not below -100
+// (the weights are summed in units of 2^e: a token's is then below 2^115).
 __device__ __forceinline__ float kv4_level(float scaled, float least) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(scaled));
   return fmaxf(y, least);
 }
-__device__ __forceinline__ float kv4_least_level(float e) { return fmaxf(-60.f - e, -100.f); }
+__device__ __forceinline__ float kv4_least_level(float e) {
+  return fmaxf(kKv4LeastExponent - e, -100.f);
+}
 
 namespace kv4_decode_cfg {
 constexpr int kThreads = 128;
