@@ -163,8 +163,9 @@ atom_status_t kv4_rows(bool append, const void *k, int64_t k_token, int64_t k_he
 }
 
 // Largest number of query rows of a KV head that goes to the first kernel of the
-// attention weights (kv4_few_rows is the attention's): 64 sequences of 8192 tokens with 8 rows 77
-// us in the first kernel; 16 of 3000, 8 heads, 24 rows 43 and 45, 32 rows 54 and 45.
+// attention weights (kv4_few_rows is the attention's). Both measured, us: 16 sequences of
+// 3000 tokens, 8 heads, 16 rows 34 and 42, 24 rows 45 and 42, 32 rows 57 and 43; four of
+// 20000, 16 rows 49 and 66, 24 rows 66 and 67, 32 rows 85 and 67.
 constexpr int kKv4WeightFewRows = 24;
 
 // Query rows a CTA of the decode kernel takes at once, 8 or 16: the smallest

@@ -29,9 +29,11 @@
 // warp-wide mma.sync, whose operands are made in registers from the loaded
 // words, with no expanded copy of a tile in shared memory (which a tcgen05
 // operand would need: twice the loaded bytes written, then read). It measures
-// 4.1 TB/s (64 sequences of up to 8192 tokens, 64 heads over 8: 419 MB in 102
-// us), with a warp's 300 instructions for 16 tokens, half of them turning codes
-// into fp16, and the twelve warps an SM that the rings leave room for.
+// 4.1 TB/s (64 sequences of up to 8192 tokens, 64 heads over 8: 419 MB in 101 us
+// in a replayed graph, 105 to 107 a call). No unit is full: DRAM 50 %, issue slots
+// 57 %, ALU 47 %, with the twelve warps an SM that the rings leave room for. A
+// warp issues 300 instructions for 16 tokens, half of them turning codes into
+// fp16; their chains of dependent steps, three warps to a scheduler, take the time.
 //
 // The products. M is the side of the tokens (first product) or of the elements
 // (second), N is the query rows, 8 per n-tile. A contraction's order is free,

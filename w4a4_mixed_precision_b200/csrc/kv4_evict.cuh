@@ -20,10 +20,11 @@
 // steps: every copy of a step is read before any is written, and a token never
 // moves up, so nothing is overwritten that is still to be read.
 //
-// What bounds it: many sequences, the bytes moved (136 read and written per
-// token and head that stays: 64 x 2048 tokens to 1024, 8 heads, 36 us, 4 TB/s);
-// one long sequence, latency: four passes and a dozen cluster barriers (65537 to
-// 4097 tokens, 8 heads, 26 us).
+// What bounds it: many sequences, the latencies of three passes and the move, for
+// DRAM is half busy (136 bytes read and written per token and head that stays: 64 x
+// 2048 tokens to 1024, 8 heads, 42 us in a replayed graph, 3.5 TB/s); one long
+// sequence, four passes and a dozen cluster barriers (65537 to 4097 tokens, 8
+// heads, 28 us).
 #pragma once
 
 #include "kv4_plan.h"

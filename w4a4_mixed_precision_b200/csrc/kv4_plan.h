@@ -126,9 +126,12 @@ KV4_HD int kv4_part_of(int64_t total, int parts, int64_t at) {
 // The decode kernel reads the cache once per 16 rows and divides that evenly over
 // the GPU: 44 us per million tokens, pair and 16 rows. The prompt kernel reads it
 // once per 256 rows, with one CTA an SM and a CTA a pair and 256 rows: 22 us per
-// thousand tokens for each round of CTAs. (Both measured: 16 sequences of 3000
-// tokens, 8 heads, 64 rows 76 and 77 us, 128 rows 139 and 78; one sequence, 512
-// rows 44 and 73.)
+// thousand tokens for each round of CTAs. (Both measured, us: 16 sequences of 3000
+// tokens, 8 heads, 32 rows 46 and 74, 64 rows 77 and 76, 128 rows 141 and 76; one
+// sequence, 512 rows 46 and 73; four of 20000, 128 rows 204 and 410, 256 rows 391
+// and 412, 512 rows 766 and 413. Neither divides the cached tokens of many rows:
+// with one KV head, 8 query heads and 1024 new tokens behind 32768 both are far
+// from the tensor cores' 83 us, 634 and 676.)
 inline int64_t kv4_few_rows(int64_t pairs, int64_t max_rows, int sms) {
   if (pairs > int64_t(1) << 40) pairs = int64_t(1) << 40;   // (the products stay in 64 bits)
   int64_t rows = 16;

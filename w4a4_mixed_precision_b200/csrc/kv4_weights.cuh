@@ -9,8 +9,9 @@
 //
 // Few query rows (single and drafted tokens), kv4_weights_kernel: a warp expands
 // the keys of 16 tokens at a time and passes the query rows that see one of them
-// by, 8 at a time. What bounds it: the instructions that expand the codes (64
-// sequences of up to 8192 tokens, 64 heads over 8: 237 MB in 63 us, 3.8 TB/s).
+// by, 8 at a time. 64 sequences of up to 8192 tokens, 64 heads over 8: 237 MB in 62
+// us in a replayed graph, 3.8 TB/s; 65 to 68 a call. No unit is full (issue slots 61
+// %, ALU 43 %, DRAM 43 %): a warp's chains of copies, expansion and products.
 //
 // Many (prompts), kv4_weights_prompt_kernel: the transposed product K Q^T on the
 // tcgen05 tensor cores. A CTA takes 128 tokens of a (sequence, KV head) and all
@@ -20,8 +21,9 @@
 // as the A operand (read from shared memory for each product, A costs 105
 // cycles a 128x128x16 MMA instead of 74). What bounds it: the exponentials, 1024
 // cycles of the SM per 128x128 tile, against 592 of the tensor core (4096 tokens,
-// 64 heads over 8: 181 us with the exponential unit 78 % busy; with an eighth to a
-// half of them as a polynomial on the FMA units 187 to 213).
+// 64 heads over 8: 180 us in a replayed graph, 188 to 192 a call, with the
+// exponential unit 79 % busy; an earlier form took 181, and with an eighth to a half
+// of them as a polynomial on the FMA units 187 to 213).
 #pragma once
 
 #include "kv4_prompt.cuh"
