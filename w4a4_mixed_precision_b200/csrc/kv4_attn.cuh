@@ -30,7 +30,7 @@
 // words, with no expanded copy of a tile in shared memory (which a tcgen05
 // operand would need: twice the loaded bytes written, then read). It measures
 // 4.1 TB/s (64 sequences of up to 8192 tokens, 64 heads over 8: 419 MB in 101 us
-// in a replayed graph, 105 to 107 a call). No unit is full: DRAM 50 %, issue slots
+// in a replayed graph, 105 to 109 a call). No unit is full: DRAM 50 %, issue slots
 // 57 %, ALU 47 %, with the twelve warps an SM that the rings leave room for. A
 // warp issues 300 instructions for 16 tokens, half of them turning codes into
 // fp16; their chains of dependent steps, three warps to a scheduler, take the time.

@@ -29,7 +29,7 @@
 //   warp 18, lane 0      finds the work items, starts the copies of their queries
 // While the tensor core multiplies for one query tile, the other tile's weights
 // are made. A prompt of 4096 tokens, 64 heads over 8, takes 321 us in a replayed
-// graph (856 TFLOP/s), 329 to 336 a call. What bounds it (parts left out in
+// graph (856 TFLOP/s), 329 to 340 a call. What bounds it (parts left out in
 // copies, of then 334 us): of the clocks of a KV tile and two query tiles, some
 // 2200, the tensor core works 1776 (74 for each instruction of S, 16 x 128 x 64,
 // which its operands' way out of shared memory costs, and 74 for each of O), the

@@ -21,7 +21,7 @@
 // as the A operand (read from shared memory for each product, A costs 105
 // cycles a 128x128x16 MMA instead of 74). What bounds it: the exponentials, 1024
 // cycles of the SM per 128x128 tile, against 592 of the tensor core (4096 tokens,
-// 64 heads over 8: 180 us in a replayed graph, 188 to 192 a call, with the
+// 64 heads over 8: 180 us in a replayed graph, 188 to 193 a call, with the
 // exponential unit 79 % busy; an earlier form took 181, and with an eighth to a half
 // of them as a polynomial on the FMA units 187 to 213).
 #pragma once
